@@ -370,6 +370,164 @@ DSA_API int dsa_index_decode_noalloc_status(uint32_t* status, void* stream);
 DSA_API int dsa_index_device_status(const void* workspace, uint32_t* status, void* stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Serving operators around the index Top-k: what a step needs before the
+ * index entry points (its pages and slots, its rotated queries and keys) and
+ * after them (attention over the selected keys).  Conventions as above, and:
+ *  - `status` is a device word of the caller's, or NULL.  A call ORs the bits
+ *    of dsa_index_device_status into it and never clears it, so one word can
+ *    collect a whole step; without it the same checks skip the same accesses
+ *    but go unreported.
+ *  - A row with position < 0, slot < 0 or sequence < 0 is padding (the rows
+ *    of a captured graph behind the last token): its outputs are left as
+ *    they were.
+ *  - None of the calls waits for the host; all can be captured into a graph.
+ *
+ * Layout of one step ("DeepSeek DSA FLOPs", Decode and Prefill: each step
+ * adds tokens behind the cached ones; the pages have no paging, the layout is
+ * dsa_index_decode_paged's).  Request b holds cached_len[b] tokens and gets
+ * new_len[b] more (0 for an idle request, 1 for decode, a chunk for prefill).
+ * The blocks that the new tokens need beyond those b already has take pages
+ * free_pages[*free_begin], free_pages[*free_begin + 1], ... in request order.
+ *   cached_len, new_len  device, [B] int32; 1 <= B <= 65536
+ *   block_table  device, [B][max_blocks] int32, updated in place: only the
+ *                entries of new blocks are written
+ *   free_pages   device, [n_free] int32 page ids; free_begin device, [1]
+ *                int32: how many of them are taken already
+ *   T_cap        rows of the three row outputs; rows past the step's last
+ *                token are -1
+ *   slot_map     device, [T_cap] int32: pool row page * page_size + offset
+ *   position     device, [T_cap] int32: position within the sequence
+ *   row_seq      device, [T_cap] int32: the row's request
+ *   row_start    device, [B + 1] int32: first row of each request, then the
+ *                number of rows
+ *   seq_len      device, [B] int32: cached_len + new_len (the lengths that
+ *                dsa_index_decode_paged takes)
+ *   free_end     device, [1] int32: the next step's free_begin
+ * All or nothing: a negative length, a request beyond max_blocks pages, more
+ * than T_cap rows or more than the free pages set status bit 1, and then no
+ * request gets new tokens (rows all -1, seq_len = cached_len, free_end =
+ * free_begin, block_table unchanged).  A page id outside [0, n_pages) gives
+ * slot -1 to the rows on it and sets bit 1.  Outputs may not alias inputs.
+ * Requires max_blocks * page_size < 2^31, n_pages * page_size < 2^31 and
+ * T_cap < 2^30.  Exact integer work.
+ */
+DSA_API int dsa_block_tables(const int32_t* cached_len, const int32_t* new_len, int B, int32_t* block_table,
+                             int max_blocks, const int32_t* free_pages, int64_t n_free, const int32_t* free_begin,
+                             int64_t n_pages, int page_size, int64_t T_cap, int32_t* slot_map, int32_t* position,
+                             int32_t* row_seq, int32_t* row_start, int32_t* seq_len, int32_t* free_end,
+                             uint32_t* status, void* stream);
+
+/*
+ * Index queries and keys of a step, normalised, rotated and stored ("DeepSeek
+ * DSA FLOPs", Lightning Indexer: the projections' outputs that the score
+ * takes).  Every head row x of width d = 128 is
+ *   DSA_NORM_NONE   left as it is
+ *   DSA_NORM_RMS    x / sqrt(mean(x^2) + eps) * weight + bias
+ *   DSA_NORM_LAYER  (x - mean(x)) / sqrt(var(x) + eps) * weight + bias
+ * (weight 1 and bias 0 where the pointer is NULL; both must be NULL without a
+ * norm), then its first `rot` dimensions are rotated: pair i by the angle
+ * position * inv_freq[i], (a, b) -> (a cos - b sin, a sin + b cos), where the
+ * pair is dimensions (2i, 2i + 1) when `interleaved`, else (i, i + rot / 2).
+ * Queries and keys have norms of their own.  Statistics and rotation are
+ * fp32, the angle is reduced in fp64 (exact to fp32 at any position); the
+ * store rounds once.
+ *   q         device, [T][H][128] bf16 (1 <= H <= 256)
+ *   k         device, [T][128] bf16
+ *   position  device, [T] int32; < 0: padding, neither row is written
+ *   inv_freq  device, [rot / 2] fp32; rot a multiple of 16 in [0, 128]
+ *   *_weight, *_bias  device, [128] fp32, 16-byte aligned, or NULL
+ *   slot_map  device, [T] int32: key t is stored at row slot_map[t] of k_out
+ *             (< 0: not stored; >= n_slots: not stored, status bit 1); NULL
+ *             stores key t at row t.  Slots must differ.
+ *   q_out     device, [T][H][128] bf16; may be q itself
+ *   k_out     device, [n_slots][128] bf16: a contiguous key cache or a page
+ *             pool [n_pages][page_size][128]
+ * T == 0 is a no-op.
+ *
+ * dsa_index_prepare_fp8 stores E4M3 codes with one fp32 scale per row, as
+ * dsa_index_prefill_fp8 takes them: scale = max|y| / 448 (1 for a row of
+ * zeros, at least 2^-126), code = E4M3(y / scale), the quotient within two
+ * fp32 roundings.  q_scale is [T][H], k_scale [n_slots].
+ */
+#define DSA_NORM_NONE 0
+#define DSA_NORM_RMS 1
+#define DSA_NORM_LAYER 2
+DSA_API int dsa_index_prepare(const uint16_t* q, const uint16_t* k, const int32_t* position, const float* inv_freq,
+                              int rot, int64_t T, int H, int d, int q_norm, const float* q_weight,
+                              const float* q_bias, int k_norm, const float* k_weight, const float* k_bias,
+                              float eps, int interleaved, const int32_t* slot_map, int64_t n_slots,
+                              uint16_t* q_out, uint16_t* k_out, uint32_t* status, void* stream);
+DSA_API int dsa_index_prepare_fp8(const uint16_t* q, const uint16_t* k, const int32_t* position,
+                                  const float* inv_freq, int rot, int64_t T, int H, int d, int q_norm,
+                                  const float* q_weight, const float* q_bias, int k_norm, const float* k_weight,
+                                  const float* k_bias, float eps, int interleaved, const int32_t* slot_map,
+                                  int64_t n_slots, uint8_t* q_out, float* q_scale, uint8_t* k_out, float* k_scale,
+                                  uint32_t* status, void* stream);
+
+/*
+ * The 4-bit latent cache of the attention ("DeepSeek DSA FLOPs", notation:
+ * d_c = 512 latent dimensions that serve as keys and values of all heads,
+ * d_r = 64 rotary dimensions).  A token is 416 bytes:
+ *   bytes   0..255  512 E2M1 codes, dimension 2i in the low nibble of byte i
+ *   bytes 256..287  32 E4M3 scales, one per 16 consecutive dimensions
+ *   bytes 288..415  64 rotary values, bf16
+ * and a latent value is code * scale.  dsa_kv4_write quantises row t into
+ * pool row slot_map[t]: scale = E4M3(max|x| / 6), code = E2M1(x / scale),
+ * both to the nearest with ties to even and saturating, both quotients in
+ * fp32 (codes are 0 where the scale is 0: a block's maximum below about
+ * 0.006); rotary values are copied.  A block's maximum keeps its precision
+ * between 0.094 and 2688.  dsa_kv4_read gives rows back in bf16 (exact).
+ *   latent    device, [T][512] bf16, 16-byte aligned; rope [T][64] bf16
+ *   kv_pages  device, [n_slots][416] bytes, 32-byte aligned: a page pool
+ *             [n_pages][page_size][416]; n_slots < 2^31
+ *   slot_map  device, [T] int32; < 0: padding; >= n_slots: skipped, status
+ *             bit 1.  The slots of a write must differ.
+ * T == 0 is a no-op.
+ */
+#define DSA_KV4_ENTRY_BYTES 416
+DSA_API int dsa_kv4_write(const uint16_t* latent, const uint16_t* rope, uint8_t* kv_pages, int64_t n_slots,
+                          const int32_t* slot_map, int64_t T, uint32_t* status, void* stream);
+DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t* slot_map, int64_t T,
+                         uint16_t* latent, uint16_t* rope, uint32_t* status, void* stream);
+
+/*
+ * Attention over the selected keys ("DeepSeek DSA FLOPs", core sparse
+ * attention: all heads of a row attend to the row's Top-k keys through one
+ * shared latent entry per token).  For row t, head h and the entries s of
+ * idx[t] (positions within the row's sequence; negative entries are skipped,
+ * an entry listed twice counts twice; the order does not matter):
+ *   z(t,h,s) = scale * (q[t][h][0..511] . latent(s) + q[t][h][512..575] . rotary(s))
+ *   out[t][h] = sum_s softmax_s(z) latent(s),   lse[t][h] = log sum_s exp z
+ * A row with no entry has out = 0 and lse = -inf.
+ *   q            device, [T][H][576] bf16, 16-byte aligned; 1 <= H <= 256
+ *   kv_pages     device, [n_pages][page_size][416] bytes (dsa_kv4_write),
+ *                32-byte aligned; page_size >= 1
+ *   block_table  device, [B][max_blocks] int32 page ids; row t reads the
+ *                table of sequence row_seq[t]
+ *   row_seq      device, [T] int32: < 0: padding, the row's outputs are left
+ *                as they were; >= B: the same, and status bit 1.  NULL: row t
+ *                reads sequence t (needs T <= B)
+ *   idx          device, [T][n] int32, n >= 1: out_idx of the index entry
+ *                points, or any other list.  An entry at or beyond
+ *                max_blocks * page_size, or on a page outside [0, n_pages),
+ *                is skipped and sets status bit 1
+ *   scale        finite
+ *   out          device, [T][H][512] bf16, 16-byte aligned
+ *   lse          device, [T][H] fp32 (natural logarithm), or NULL
+ *   workspace    device, 256-byte aligned, of
+ *                dsa_attend_kv4_workspace_bytes(T, H, n) bytes
+ * Scores, softmax statistics and output sums are fp32.  Results do not depend
+ * on the rest of the batch's contents.  T == 0 is a no-op.  Requires
+ * max_blocks * page_size < 2^31, n_pages * page_size < 2^31, T * H < 2^31.
+ */
+DSA_API size_t dsa_attend_kv4_workspace_bytes(int64_t T, int H, int n);
+DSA_API int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n_pages, int page_size,
+                           const int32_t* block_table, int B, int max_blocks, const int32_t* row_seq,
+                           const int32_t* idx, int64_t T, int H, int n, float scale, uint16_t* out, float* lse,
+                           void* workspace, size_t ws_bytes, uint32_t* status, void* stream);
+
+/*
  * Failure injection for tests of the bounded device waits (no counterpart on
  * the pages).  Arms a one-shot fault for the calling host thread: the next
  * fused scoring launch of any entry point issues no loads, so its MMA warp

@@ -26,6 +26,8 @@ __all__ = [
     "dsa_index_seeds_from_history", "dsa_index_seeds_from_history_workspace_bytes",
     "dsa_index_prefill_paged", "dsa_index_prefill_paged_workspace_bytes",
     "dsa_index_prefill_pruned_paged", "dsa_index_prefill_pruned_paged_workspace_bytes",
+    "dsa_block_tables", "dsa_index_prepare", "dsa_index_prepare_fp8", "dsa_kv4_write", "dsa_kv4_read",
+    "dsa_attend_kv4", "dsa_attend_kv4_workspace_bytes",
 ]
 
 DSA_OK = 0
@@ -91,6 +93,21 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
         L.dsa_index_seeds_from_history_workspace_bytes.restype = SZ
         L.dsa_index_seeds_from_history.argtypes = [P, I64, I, I64, I, P, P, SZ, P]
         L.dsa_index_seeds_from_history.restype = I
+        L.dsa_block_tables.argtypes = [P, P, I, P, I, P, I64, P, I64, I, I64, P, P, P, P, P, P, P, P]
+        L.dsa_block_tables.restype = I
+        F = ctypes.c_float
+        L.dsa_index_prepare.argtypes = [P, P, P, P, I, I64, I, I, I, P, P, I, P, P, F, I, P, I64, P, P, P, P]
+        L.dsa_index_prepare.restype = I
+        L.dsa_index_prepare_fp8.argtypes = [P, P, P, P, I, I64, I, I, I, P, P, I, P, P, F, I, P, I64, P, P, P, P, P, P]
+        L.dsa_index_prepare_fp8.restype = I
+        L.dsa_kv4_write.argtypes = [P, P, P, I64, P, I64, P, P]
+        L.dsa_kv4_write.restype = I
+        L.dsa_kv4_read.argtypes = [P, I64, P, I64, P, P, P, P]
+        L.dsa_kv4_read.restype = I
+        L.dsa_attend_kv4_workspace_bytes.argtypes = [I64, I, I]
+        L.dsa_attend_kv4_workspace_bytes.restype = SZ
+        L.dsa_attend_kv4.argtypes = [P, P, I64, I, P, I, I, P, P, I64, I, I, F, P, P, P, SZ, P, P]
+        L.dsa_attend_kv4.restype = I
         L.dsa_index_decode_noalloc.argtypes = [P, P, P, P, I, I64, I, I, I, P, P, P]
         L.dsa_index_decode_noalloc.restype = I
         L.dsa_index_decode_noalloc_status.argtypes = [P, P]
@@ -526,6 +543,235 @@ def dsa_index_decode_noalloc_status(device=None) -> int:
     with torch.cuda.device(dev):
         _check(lib().dsa_index_decode_noalloc_status(ctypes.byref(st), _stream_ptr(dev)))
     return int(st.value)
+
+
+# ---------------------------------------------------------------------------
+# Serving operators around the index Top-k.  `status`, where a call takes it,
+# is an int32 tensor (1,) on the device, or None: the call ORs the bits of
+# dsa_index_device_status into it and never clears it.
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+KV4_ENTRY_BYTES = 416
+KV4_LATENT, KV4_ROPE = 512, 64
+
+
+def _opt(t, name: str, dtype, shape: tuple, device) -> int | None:
+    """Pointer of an optional contiguous tensor of exactly this shape."""
+    if t is None:
+        return None
+    _need(t, name, dtype, len(shape), device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _out(t, name: str, dtype, shape: tuple, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _opt(t, name, dtype, shape, device)
+    return t
+
+
+def dsa_block_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
+                     free_pages: torch.Tensor, free_begin: torch.Tensor, n_pages: int, page_size: int, T_cap: int,
+                     slot_map=None, position=None, row_seq=None, row_start=None, seq_len=None, free_end=None,
+                     status=None):
+    """Pages, cache slots, positions and owners of one step's new tokens.
+
+    cached_len, new_len (B,) int32; block_table (B, max_blocks) int32, whose
+    entries of newly needed blocks are filled in place from free_pages
+    (n_free,) int32, starting at free_begin (1,) int32; T_cap rows.  Returns
+    (slot_map, position, row_seq, row_start, seq_len, free_end), all int32:
+    (T_cap,) three times, -1 past the last token, then (B + 1,), (B,), (1,).
+    When a length is out of range or rows or pages do not suffice, no request
+    gets new tokens and status bit 1 is set.
+    """
+    dev = block_table.device
+    _need(cached_len, "cached_len", torch.int32, 1, dev)
+    B = cached_len.shape[0]
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(free_pages, "free_pages", torch.int32, 1, dev)
+    _opt(new_len, "new_len", torch.int32, (B,), dev)
+    _opt(free_begin, "free_begin", torch.int32, (1,), dev)
+    if new_len is None or free_begin is None or block_table.shape[0] != B:
+        raise ValueError("need new_len (B,), free_begin (1,) and block_table (B, max_blocks)")
+    T_cap = int(T_cap)
+    if T_cap < 0:
+        raise ValueError("T_cap must not be negative")
+    slot_map = _out(slot_map, "slot_map", torch.int32, (T_cap,), dev)
+    position = _out(position, "position", torch.int32, (T_cap,), dev)
+    row_seq = _out(row_seq, "row_seq", torch.int32, (T_cap,), dev)
+    row_start = _out(row_start, "row_start", torch.int32, (B + 1,), dev)
+    seq_len = _out(seq_len, "seq_len", torch.int32, (B,), dev)
+    free_end = _out(free_end, "free_end", torch.int32, (1,), dev)
+    st = _opt(status, "status", torch.int32, (1,), dev)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_block_tables(cached_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
+                                      block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+                                      free_begin.data_ptr(), int(n_pages), int(page_size), T_cap,
+                                      slot_map.data_ptr(), position.data_ptr(), row_seq.data_ptr(),
+                                      row_start.data_ptr(), seq_len.data_ptr(), free_end.data_ptr(), st,
+                                      _stream_ptr(dev)))
+    return slot_map, position, row_seq, row_start, seq_len, free_end
+
+
+def _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight, q_bias, k_norm, k_weight, k_bias, status):
+    dev = q.device
+    _need(q, "q", torch.bfloat16, 3, dev)
+    T, H, d = q.shape
+    _need(k, "k", torch.bfloat16, 2, dev)
+    if tuple(k.shape) != (T, d):
+        raise ValueError("shape mismatch between q (T,H,d) and k (T,d)")
+    _need(position, "position", torch.int32, 1, dev)
+    _need(inv_freq, "inv_freq", torch.float32, 1, dev)
+    if position.shape[0] != T:
+        raise ValueError(f"position must be ({T},)")
+    if k_out.dim() < 2 or k_out.shape[-1] != d:
+        raise ValueError(f"k_out must hold rows of {d}: (n_slots, {d}) or (n_pages, page_size, {d})")
+    for name in (q_norm, k_norm):
+        if name not in NORMS:
+            raise ValueError(f"norm must be one of {sorted(NORMS)}, got {name!r}")
+    w = [_opt(t, n, torch.float32, (d,), dev) for t, n in
+         ((q_weight, "q_weight"), (q_bias, "q_bias"), (k_weight, "k_weight"), (k_bias, "k_bias"))]
+    head = (q.data_ptr(), k.data_ptr(), position.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], T, H, d,
+            NORMS[q_norm], w[0], w[1], NORMS[k_norm], w[2], w[3])
+    slots = (_opt(slot_map, "slot_map", torch.int32, (T,), dev), k_out.numel() // d)
+    return dev, T, H, d, head, slots, _opt(status, "status", torch.int32, (1,), dev)
+
+
+def dsa_index_prepare(q: torch.Tensor, k: torch.Tensor, position: torch.Tensor, inv_freq: torch.Tensor,
+                      k_out: torch.Tensor, slot_map=None, q_norm: str = "none", q_weight=None, q_bias=None,
+                      k_norm: str = "none", k_weight=None, k_bias=None, eps: float = 1e-6,
+                      interleaved: bool = False, q_out=None, status=None):
+    """Norm and position rotation of index queries and keys in one pass, keys
+    stored at their cache slots.
+
+    q (T, H, 128) bf16, k (T, 128) bf16, position (T,) int32, inv_freq
+    (rot / 2,) fp32; norms are "none", "rms" or "layer" with weight and bias
+    (128,) fp32.  Key t goes to row slot_map[t] (t without slot_map) of k_out,
+    bf16 rows of 128: (n_slots, 128) or a page pool (n_pages, page_size, 128).
+    Rows with position < 0 are padding and left as they were.  Returns
+    (q_out (T, H, 128) bf16, k_out); q_out may be q.
+    """
+    dev, T, H, d, head, slots, st = _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight,
+                                                  q_bias, k_norm, k_weight, k_bias, status)
+    _need(k_out, "k_out", torch.bfloat16, k_out.dim(), dev)
+    q_out = _out(q_out, "q_out", torch.bfloat16, (T, H, d), dev)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_index_prepare(*head, float(eps), int(bool(interleaved)), *slots, q_out.data_ptr(),
+                                       k_out.data_ptr(), st, _stream_ptr(dev)))
+    return q_out, k_out
+
+
+def dsa_index_prepare_fp8(q: torch.Tensor, k: torch.Tensor, position: torch.Tensor, inv_freq: torch.Tensor,
+                          k_out: torch.Tensor, k_scale_out: torch.Tensor, slot_map=None, q_norm: str = "none",
+                          q_weight=None, q_bias=None, k_norm: str = "none", k_weight=None, k_bias=None,
+                          eps: float = 1e-6, interleaved: bool = False, q_out=None, q_scale_out=None, status=None):
+    """dsa_index_prepare with E4M3 codes and one fp32 scale per row as output,
+    the inputs of dsa_index_prefill_fp8.  Returns (q_out (T, H, 128), q_scale
+    (T, H), k_out (..., 128), k_scale_out (...,)); codes are uint8 or
+    float8_e4m3fn tensors."""
+    dev, T, H, d, head, slots, st = _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight,
+                                                  q_bias, k_norm, k_weight, k_bias, status)
+    kc = _codes(k_out, "k_out", k_out.dim(), dev)
+    ks = _opt(k_scale_out, "k_scale_out", torch.float32, tuple(k_out.shape[:-1]), dev)
+    q_out = torch.empty((T, H, d), dtype=torch.uint8, device=dev) if q_out is None else q_out
+    qc = _codes(q_out, "q_out", 3, dev)
+    if tuple(qc.shape) != (T, H, d):
+        raise ValueError(f"q_out must be {(T, H, d)}")
+    q_scale_out = _out(q_scale_out, "q_scale_out", torch.float32, (T, H), dev)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_index_prepare_fp8(*head, float(eps), int(bool(interleaved)), *slots, qc.data_ptr(),
+                                           q_scale_out.data_ptr(), kc.data_ptr(), ks, st, _stream_ptr(dev)))
+    return q_out, q_scale_out, k_out, k_scale_out
+
+
+def _kv4_pool(kv_pages, dev):
+    _need(kv_pages, "kv_pages", torch.uint8, 3, dev)
+    if kv_pages.shape[2] != KV4_ENTRY_BYTES:
+        raise ValueError(f"kv_pages must be (n_pages, page_size, {KV4_ENTRY_BYTES}), got {tuple(kv_pages.shape)}")
+    return kv_pages.shape[0] * kv_pages.shape[1]
+
+
+def dsa_kv4_write(latent: torch.Tensor, rope: torch.Tensor, kv_pages: torch.Tensor, slot_map: torch.Tensor,
+                  status=None) -> torch.Tensor:
+    """Quantise tokens into the 4-bit latent cache.
+
+    latent (T, 512) bf16, rope (T, 64) bf16; token t goes to row slot_map[t]
+    (int32; < 0: padding) of the page pool kv_pages (n_pages, page_size, 416)
+    uint8.  Returns kv_pages.
+    """
+    dev = kv_pages.device
+    n_slots = _kv4_pool(kv_pages, dev)
+    _need(latent, "latent", torch.bfloat16, 2, dev)
+    T = latent.shape[0]
+    if latent.shape[1] != KV4_LATENT:
+        raise ValueError(f"latent must be (T, {KV4_LATENT})")
+    _need(rope, "rope", torch.bfloat16, 2, dev)
+    _need(slot_map, "slot_map", torch.int32, 1, dev)
+    if tuple(rope.shape) != (T, KV4_ROPE) or slot_map.shape[0] != T:
+        raise ValueError(f"rope must be ({T}, {KV4_ROPE}) and slot_map ({T},)")
+    st = _opt(status, "status", torch.int32, (1,), dev)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_kv4_write(latent.data_ptr(), rope.data_ptr(), kv_pages.data_ptr(), n_slots,
+                                   slot_map.data_ptr(), T, st, _stream_ptr(dev)))
+    return kv_pages
+
+
+def dsa_kv4_read(kv_pages: torch.Tensor, slot_map: torch.Tensor, latent_out=None, rope_out=None, status=None):
+    """Rows slot_map (T,) int32 of the 4-bit latent cache in bf16 (exact):
+    (latent (T, 512), rope (T, 64)).  Rows with a slot < 0 are left as they
+    were."""
+    dev = kv_pages.device
+    n_slots = _kv4_pool(kv_pages, dev)
+    _need(slot_map, "slot_map", torch.int32, 1, dev)
+    T = slot_map.shape[0]
+    latent_out = _out(latent_out, "latent_out", torch.bfloat16, (T, KV4_LATENT), dev)
+    rope_out = _out(rope_out, "rope_out", torch.bfloat16, (T, KV4_ROPE), dev)
+    st = _opt(status, "status", torch.int32, (1,), dev)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_kv4_read(kv_pages.data_ptr(), n_slots, slot_map.data_ptr(), T, latent_out.data_ptr(),
+                                  rope_out.data_ptr(), st, _stream_ptr(dev)))
+    return latent_out, rope_out
+
+
+def dsa_attend_kv4_workspace_bytes(T: int, H: int, n: int) -> int:
+    return int(lib().dsa_attend_kv4_workspace_bytes(int(T), int(H), int(n)))
+
+
+def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.Tensor, idx: torch.Tensor,
+                   scale: float, row_seq=None, out=None, lse=None, workspace=None, status=None):
+    """Attention of every head over the row's selected keys of a 4-bit latent
+    cache.
+
+    q (T, H, 576) bf16 (512 latent, 64 rotary dimensions), kv_pages (n_pages,
+    page_size, 416) uint8 (dsa_kv4_write), block_table (B, max_blocks) int32,
+    idx (T, n) int32: positions within the row's sequence (out_idx of the
+    index calls), negative entries skipped.  row_seq (T,) int32 names each
+    row's sequence (< 0: padding, left as it was); without it row t reads
+    sequence t.  Returns (out (T, H, 512) bf16, lse (T, H) fp32).
+    """
+    dev = kv_pages.device
+    _kv4_pool(kv_pages, dev)
+    _need(q, "q", torch.bfloat16, 3, dev)
+    T, H, dq = q.shape
+    _need(block_table, "block_table", torch.int32, 2, dev)
+    _need(idx, "idx", torch.int32, 2, dev)
+    B, max_blocks = block_table.shape
+    if dq != KV4_LATENT + KV4_ROPE or idx.shape[0] != T:
+        raise ValueError(f"need q (T, H, {KV4_LATENT + KV4_ROPE}) and idx (T, n)")
+    n = idx.shape[1]
+    rs = _opt(row_seq, "row_seq", torch.int32, (T,), dev)
+    out = _out(out, "out", torch.bfloat16, (T, H, KV4_LATENT), dev)
+    lse = _out(lse, "lse", torch.float32, (T, H), dev)
+    st = _opt(status, "status", torch.int32, (1,), dev)
+    ws = _workspace(dsa_attend_kv4_workspace_bytes(T, H, n), dev, workspace)
+    with torch.cuda.device(dev):
+        _check(lib().dsa_attend_kv4(q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0], kv_pages.shape[1],
+                                    block_table.data_ptr(), B, max_blocks, rs, idx.data_ptr(), T, H, n, float(scale),
+                                    out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), st,
+                                    _stream_ptr(dev)))
+    return out, lse
 
 
 def dsa_test_inject_wait_timeout(limit_ns: int) -> None:

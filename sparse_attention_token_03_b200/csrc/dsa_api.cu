@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -18,6 +19,7 @@
 #include "dsa_dosa.cuh"
 #include "dsa_kernels.cuh"
 #include "dsa_ptx.cuh"
+#include "dsa_serve.cuh"
 
 using namespace dsa;
 
@@ -788,6 +790,75 @@ void take_wait_injection(ScoreParams& p) {
 }
 }  // namespace dsa
 
+namespace {
+
+// Page pool and block table sizes of the serving operators.
+int check_pool(int64_t n_pages, int page_size, int max_blocks) {
+  if (n_pages < 1 || page_size < 1 || max_blocks < 1)
+    return fail(DSA_EINVAL, "need n_pages >= 1, page_size >= 1 and max_blocks >= 1");
+  if (n_pages >= (int64_t(1) << 31) || n_pages * page_size >= (int64_t(1) << 31))
+    return fail(DSA_EINVAL, "n_pages * page_size must be below 2^31");
+  if (static_cast<int64_t>(max_blocks) * page_size >= (int64_t(1) << 31))
+    return fail(DSA_EINVAL, "max_blocks * page_size must be below 2^31");
+  return DSA_OK;
+}
+
+int check_attend_shape(int64_t T, int H, int n) {
+  if (H < 1 || H > 256) return fail(DSA_EUNSUPPORTED, "H = %d outside [1, 256]", H);
+  if (n < 1) return fail(DSA_EINVAL, "need n >= 1 entries per list");
+  if (T < 0 || T >= (int64_t(1) << 31) / H) return fail(DSA_EINVAL, "need 0 <= T and T * H < 2^31");
+  return DSA_OK;
+}
+
+int prepare_run(const PrepareParams& p, int d, void* stream) {
+  if (d != kD) return fail(DSA_EUNSUPPORTED, "d = %d: only d = 128 is supported", d);
+  if (p.H < 1 || p.H > 256) return fail(DSA_EUNSUPPORTED, "H = %d outside [1, 256]", p.H);
+  if (p.rot < 0 || p.rot > kD || p.rot % 16 != 0)
+    return fail(DSA_EUNSUPPORTED, "rot = %d: need a multiple of 16 in [0, 128]", p.rot);
+  for (int norm : {p.q_norm, p.k_norm})
+    if (norm != DSA_NORM_NONE && norm != DSA_NORM_RMS && norm != DSA_NORM_LAYER)
+      return fail(DSA_EUNSUPPORTED, "norm %d is none of DSA_NORM_NONE, DSA_NORM_RMS, DSA_NORM_LAYER", norm);
+  if ((p.q_norm == DSA_NORM_NONE && (p.q_weight || p.q_bias)) || (p.k_norm == DSA_NORM_NONE && (p.k_weight || p.k_bias)))
+    return fail(DSA_EINVAL, "weight or bias without a norm");
+  if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return fail(DSA_EINVAL, "eps must be finite and not negative");
+  if (p.T < 0 || p.T >= (int64_t(1) << 31) / (p.H + 1) || p.n_slots < 0 || p.n_slots >= (int64_t(1) << 31))
+    return fail(DSA_EINVAL, "need T >= 0, T * (H + 1) < 2^31 and 0 <= n_slots < 2^31");
+  if (!p.slot_map && p.n_slots < p.T) return fail(DSA_EINVAL, "need n_slots >= T without slot_map");
+  if (p.T == 0) return DSA_OK;
+  if (!p.q || !p.k || !p.position || (p.rot > 0 && !p.inv_freq) || !p.q_out || (p.n_slots > 0 && !p.k_out) ||
+      (p.fp8 && (!p.q_scale || (p.n_slots > 0 && !p.k_scale))))
+    return fail(DSA_EINVAL, "null pointer argument");
+  if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.q_out, 16) || !aligned(p.k_out, 16) ||
+      !aligned(p.q_weight, 16) || !aligned(p.q_bias, 16) || !aligned(p.k_weight, 16) || !aligned(p.k_bias, 16) ||
+      !aligned(p.position, 4) || !aligned(p.inv_freq, 4) || !aligned(p.slot_map, 4) || !aligned(p.q_scale, 4) ||
+      !aligned(p.k_scale, 4) || !aligned(p.status, 4))
+    return fail(DSA_EINVAL, "misaligned pointer (rows, weights and biases need 16 bytes)");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(st);
+  cudaError_t e = launch_index_prepare(p, sm_count(), st);
+  if (e != cudaSuccess) return cuda_fail(e, "index preparation launch");
+  prof_mark(st, "index_prepare");
+  return DSA_OK;
+}
+
+int kv4_run(const Kv4Params& p, const uint16_t* latent, const uint16_t* rope, bool write, void* stream) {
+  if (p.T < 0 || p.T >= (int64_t(1) << 31) || p.n_slots < 0 || p.n_slots >= (int64_t(1) << 31))
+    return fail(DSA_EINVAL, "need 0 <= T < 2^31 and 0 <= n_slots < 2^31");
+  if (p.T == 0) return DSA_OK;
+  if (!latent || !rope || !p.slot_map || (p.n_slots > 0 && !p.kv)) return fail(DSA_EINVAL, "null pointer argument");
+  if (!aligned(latent, 16) || !aligned(rope, 4) || !aligned(p.kv, 32) || !aligned(p.slot_map, 4) ||
+      !aligned(p.status, 4))
+    return fail(DSA_EINVAL, "misaligned pointer (latent needs 16 bytes, kv_pages 32)");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(st);
+  cudaError_t e = write ? launch_kv4_write(p, sm_count(), st) : launch_kv4_read(p, sm_count(), st);
+  if (e != cudaSuccess) return cuda_fail(e, "latent cache launch");
+  prof_mark(st, write ? "kv4_write" : "kv4_read");
+  return DSA_OK;
+}
+
+}  // namespace
+
 extern "C" {
 
 int dsa_test_inject_wait_timeout(int64_t limit_ns) {
@@ -1365,6 +1436,117 @@ int dsa_index_decode_noalloc_status(uint32_t* status, void* stream) {
   cudaError_t e = cudaMemcpyAsync(status, ws, 4, cudaMemcpyDeviceToHost, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return cuda_fail(e, "reading the static scratch's device status word");
+  return DSA_OK;
+}
+
+int dsa_block_tables(const int32_t* cached_len, const int32_t* new_len, int B, int32_t* block_table, int max_blocks,
+                     const int32_t* free_pages, int64_t n_free, const int32_t* free_begin, int64_t n_pages,
+                     int page_size, int64_t T_cap, int32_t* slot_map, int32_t* position, int32_t* row_seq,
+                     int32_t* row_start, int32_t* seq_len, int32_t* free_end, uint32_t* status, void* stream) {
+  int rc = check_pool(n_pages, page_size, max_blocks);
+  if (rc != DSA_OK) return rc;
+  if (B < 1 || B > 65536) return fail(DSA_EINVAL, "need 1 <= B <= 65536");
+  if (T_cap < 0 || T_cap >= (int64_t(1) << 30)) return fail(DSA_EINVAL, "need 0 <= T_cap < 2^30");
+  if (n_free < 0 || n_free > INT32_MAX) return fail(DSA_EINVAL, "need 0 <= n_free < 2^31");
+  if (!cached_len || !new_len || !block_table || !free_begin || !row_start || !seq_len || !free_end ||
+      (n_free > 0 && !free_pages) || (T_cap > 0 && (!slot_map || !position || !row_seq)))
+    return fail(DSA_EINVAL, "null pointer argument");
+  for (const void* ptr : {static_cast<const void*>(cached_len), static_cast<const void*>(new_len),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_begin), static_cast<const void*>(slot_map),
+                          static_cast<const void*>(position), static_cast<const void*>(row_seq),
+                          static_cast<const void*>(row_start), static_cast<const void*>(seq_len),
+                          static_cast<const void*>(free_end), static_cast<const void*>(status)})
+    if (!aligned(ptr, 4)) return fail(DSA_EINVAL, "misaligned pointer (4 bytes)");
+  if (free_end == free_begin || seq_len == cached_len || seq_len == new_len)
+    return fail(DSA_EINVAL, "an output aliases an input");
+  TablesParams p{};
+  p.cached_len = cached_len;
+  p.new_len = new_len;
+  p.B = B;
+  p.block_table = block_table;
+  p.max_blocks = max_blocks;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.free_begin = free_begin;
+  p.n_pages = n_pages;
+  p.page_size = page_size;
+  p.T_cap = static_cast<int>(T_cap);
+  p.slot_map = slot_map;
+  p.position = position;
+  p.row_seq = row_seq;
+  p.row_start = row_start;
+  p.seq_len = seq_len;
+  p.free_end = free_end;
+  p.status = status;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(st);
+  cudaError_t e = launch_block_tables(p, st);
+  if (e != cudaSuccess) return cuda_fail(e, "block table launch");
+  prof_mark(st, "block_tables");
+  return DSA_OK;
+}
+
+int dsa_index_prepare(const uint16_t* q, const uint16_t* k, const int32_t* position, const float* inv_freq, int rot,
+                      int64_t T, int H, int d, int q_norm, const float* q_weight, const float* q_bias, int k_norm,
+                      const float* k_weight, const float* k_bias, float eps, int interleaved,
+                      const int32_t* slot_map, int64_t n_slots, uint16_t* q_out, uint16_t* k_out, uint32_t* status,
+                      void* stream) {
+  PrepareParams p{q, k, position, inv_freq, rot, interleaved, T, H, q_norm, k_norm, q_weight, q_bias, k_weight,
+                  k_bias, eps, slot_map, n_slots, q_out, nullptr, k_out, nullptr, status, false};
+  return prepare_run(p, d, stream);
+}
+
+int dsa_index_prepare_fp8(const uint16_t* q, const uint16_t* k, const int32_t* position, const float* inv_freq,
+                          int rot, int64_t T, int H, int d, int q_norm, const float* q_weight, const float* q_bias,
+                          int k_norm, const float* k_weight, const float* k_bias, float eps, int interleaved,
+                          const int32_t* slot_map, int64_t n_slots, uint8_t* q_out, float* q_scale, uint8_t* k_out,
+                          float* k_scale, uint32_t* status, void* stream) {
+  PrepareParams p{q, k, position, inv_freq, rot, interleaved, T, H, q_norm, k_norm, q_weight, q_bias, k_weight,
+                  k_bias, eps, slot_map, n_slots, q_out, q_scale, k_out, k_scale, status, true};
+  return prepare_run(p, d, stream);
+}
+
+int dsa_kv4_write(const uint16_t* latent, const uint16_t* rope, uint8_t* kv_pages, int64_t n_slots,
+                  const int32_t* slot_map, int64_t T, uint32_t* status, void* stream) {
+  Kv4Params p{latent, rope, nullptr, nullptr, kv_pages, slot_map, T, n_slots, status};
+  return kv4_run(p, latent, rope, true, stream);
+}
+
+int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t* slot_map, int64_t T, uint16_t* latent,
+                 uint16_t* rope, uint32_t* status, void* stream) {
+  Kv4Params p{nullptr, nullptr, latent, rope, const_cast<uint8_t*>(kv_pages), slot_map, T, n_slots, status};
+  return kv4_run(p, latent, rope, false, stream);
+}
+
+size_t dsa_attend_kv4_workspace_bytes(int64_t T, int H, int n) {
+  if (check_attend_shape(T, H, n) != DSA_OK) return 0;
+  return 256;
+}
+
+int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n_pages, int page_size,
+                   const int32_t* block_table, int B, int max_blocks, const int32_t* row_seq, const int32_t* idx,
+                   int64_t T, int H, int n, float scale, uint16_t* out, float* lse, void* workspace,
+                   size_t ws_bytes, uint32_t* status, void* stream) {
+  int rc = check_attend_shape(T, H, n);
+  if (rc == DSA_OK) rc = check_pool(n_pages, page_size, max_blocks);
+  if (rc != DSA_OK) return rc;
+  if (!std::isfinite(scale)) return fail(DSA_EINVAL, "scale must be finite");
+  if (T == 0) return DSA_OK;
+  if (B < 1 || (!row_seq && T > B)) return fail(DSA_EINVAL, "need B >= 1, and T <= B without row_seq");
+  if (!q || !kv_pages || !block_table || !idx || !out || !workspace) return fail(DSA_EINVAL, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(kv_pages, 32) || !aligned(out, 16) || !aligned(block_table, 4) ||
+      !aligned(row_seq, 4) || !aligned(idx, 4) || !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 256))
+    return fail(DSA_EINVAL, "misaligned pointer (q and out need 16 bytes, kv_pages 32, the workspace 256)");
+  const size_t need = dsa_attend_kv4_workspace_bytes(T, H, n);
+  if (ws_bytes < need) return fail(DSA_EWORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  AttendParams p{q, kv_pages, n_pages, page_size, block_table, B, max_blocks, row_seq, idx, T, H, n, scale, out, lse,
+                 status};
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(st);
+  cudaError_t e = launch_attend_kv4(p, sm_count(), st);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  prof_mark(st, "attend_kv4");
   return DSA_OK;
 }
 
