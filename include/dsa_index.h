@@ -508,7 +508,7 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  *   row_seq      device, [T] int32: < 0: padding, the row's outputs are left
  *                as they were; >= B: the same, and status bit 1.  NULL: row t
  *                reads sequence t (needs T <= B)
- *   idx          device, [T][n] int32, n >= 1: out_idx of the index entry
+ *   idx          device, [T][n] int32, 1 <= n <= 2^30: out_idx of the index entry
  *                points, or any other list.  An entry at or beyond
  *                max_blocks * page_size, or on a page outside [0, n_pages),
  *                is skipped and sets status bit 1

@@ -805,7 +805,7 @@ int check_pool(int64_t n_pages, int page_size, int max_blocks) {
 
 int check_attend_shape(int64_t T, int H, int n) {
   if (H < 1 || H > 256) return fail(DSA_EUNSUPPORTED, "H = %d outside [1, 256]", H);
-  if (n < 1) return fail(DSA_EINVAL, "need n >= 1 entries per list");
+  if (n < 1 || n > (1 << 30)) return fail(DSA_EINVAL, "need 1 <= n <= 2^30 entries per list");
   if (T < 0 || T >= (int64_t(1) << 31) / H) return fail(DSA_EINVAL, "need 0 <= T and T * H < 2^31");
   return DSA_OK;
 }
@@ -1521,7 +1521,7 @@ int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t* slot_m
 
 size_t dsa_attend_kv4_workspace_bytes(int64_t T, int H, int n) {
   if (check_attend_shape(T, H, n) != DSA_OK) return 0;
-  return 256;
+  return attend_workspace_bytes(T, H, n, sm_count());
 }
 
 int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n_pages, int page_size,
@@ -1544,7 +1544,7 @@ int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n_pages, 
                  status};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(st);
-  cudaError_t e = launch_attend_kv4(p, sm_count(), st);
+  cudaError_t e = launch_attend_kv4(p, workspace, sm_count(), st);
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   prof_mark(st, "attend_kv4");
   return DSA_OK;

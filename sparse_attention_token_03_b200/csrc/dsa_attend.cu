@@ -4,12 +4,44 @@
 //   z(t,h,j) = scale * (q(t,h) . [latent_j, rotary_j])
 //   out(t,h) = sum_j softmax_j(z) latent_j,   lse(t,h) = log sum_j exp z
 //
-// One block per (row, 8 heads), one warp per head: 32 keys at a time are
-// decoded to fp32 in shared memory; a lane scores one key, then holds 16
-// output dimensions; running maximum and sum in fp32.
+// A block works on one row, up to 64 of its heads and a range of its list, in
+// tiles of 64 keys.  Both products have the keys' or the latent dimensions as
+// the MMA's rows and the heads as its columns,
+//
+//   S^T [64 keys x heads]  = K [64 x 576] Q^T         (M = 64,  36 K steps)
+//   O^T [512 x heads]     += V^T [512 x 64] P^T       (M = 128, 4 x 4 K steps)
+//
+// so that O^T of 64 heads takes 256 of the 512 TMEM columns (heads as rows
+// would fill all of them with O alone) and 8 or 16 heads cost no more than
+// their columns.  K and V are the same decoded tile: 64-dimension column
+// blocks of [64 keys][128 bytes] with the 128-byte swizzle, read K-major for
+// S and M-major for O.
+//
+//   warps 0-3   softmax and output: S^T from TMEM, exp2, P^T to shared memory
+//   warps 4-11  gather and decode: four lanes per key load its 416 bytes one
+//               tile ahead into registers, E2M1 -> fp16 times the block scale
+//               (exact), and store the swizzled tile, two tile buffers
+//   warp 12     issues the MMAs
+//
+// A tile buffer is handed over in four parts of 128 dimensions, both ways:
+// O^T's product over a part frees it, so the next tile's decoding and scores
+// follow part by part.
+//
+// Numbers: the latents are exact in fp16 (code x scale has 6 significant
+// bits, 2^-10 .. 2688).  Queries go to fp16 too, each row scaled by the power
+// of two that puts its largest magnitude in [2^14, 2^15): bf16's 8 bits fit,
+// and only values below 2^-28 of that maximum round, to 2^-39 of it.  The
+// rotary parts multiply as bf16 (same power of two, exact).  P is fp16, 2^-11
+// relative (bf16's 2^-8 would double the output's error).  exp2 is taken
+// relative to a reference per head that follows the running maximum from at
+// most 2^8 below, so P stays at most 256 and O^T in TMEM is rescaled only
+// when a tile passes that, which ordinary score distributions do in the first
+// tile alone.  Scores, sums and O^T are fp32.
+//
+// Few rows: the list is split over blocks, each writes its fp32 O and (m, l),
+// and a second kernel joins them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -21,117 +53,648 @@ namespace dsa {
 
 namespace {
 
-constexpr int kAttThreads = 256;
-constexpr int kAttHeads = kAttThreads / 32;
-constexpr int kAttKeys = 32;
-constexpr int kAttPitch = kKvQ + 1;
+constexpr int kKt = 64;                          // keys per tile
+constexpr int kBlocks = kKvQ / 64;               // 64-dimension column blocks: 8 latent, 1 rotary
+constexpr int kParts = kKvLat / 128;             // hand-over parts of a tile buffer
+constexpr uint32_t kBlockBytes = kKt * 128;      // one column block
+constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
+constexpr int kSoftWarps = 4, kLoadWarps = 8;
+constexpr int kAttThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr float kRise = 8.f;                     // log2 of the largest P before the reference moves
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int NH>
+struct AttSmem {
+  static constexpr uint32_t q_block = NH * 128;
+  static constexpr uint32_t off_k = kBlocks * q_block;
+  static constexpr uint32_t off_p = off_k + 2 * kTileBytes;
+  static constexpr uint32_t off_c = off_p + kKt * 128;   // per head: factor of a score in log2 units
+  static constexpr uint32_t off_f = off_c + NH * 4;      // per head: rescaling factor, then 1 / sum
+  static constexpr uint32_t off_mask = off_f + NH * 4;   // per tile buffer: one bit per key
+  static constexpr uint32_t off_bars = off_mask + 16;
+  // part full and empty [2 buffers][4], scores [2], weights, output, drain
+  static constexpr uint32_t n_bars = 4 * kParts + 2 + 3;
+  static constexpr uint32_t off_misc = off_bars + 8 * n_bars;
+  static constexpr uint32_t bytes = off_misc + 16;
+  static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
+};
+static_assert(AttSmem<64>::request <= 227u * 1024u, "shared memory budget");
+
+// One row, head block and list range of the grid.
+struct AttGrid {
+  int head_blocks, splits, tiles;  // tiles: of a whole list
+  float* part_o;                   // [T][head_blocks][splits][NH][512]
+  float2* part_ml;                 // [T][head_blocks][splits][NH]
+  uint32_t* err;
+};
+
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
+  // M- or N-major operand: rows of 64 consecutive M (N) elements, 8 K rows per
+  // 1024-byte atom; mn_stride between 64-element groups, 1024 between K groups
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptors (kind::f16, fp32 accumulation): operand format 0 =
+// fp16, 1 = bf16; bits 15 and 16 mark M- and N-major operands.
+constexpr uint32_t idesc_att(int M, int N, uint32_t fmt, uint32_t mn_major) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (mn_major << 15) | (mn_major << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 lanes x NH columns of fp32: thread i holds rows i / 4 (values 4j, 4j + 1)
+// and i / 4 + 8 (4j + 2, 4j + 3) at columns 8j + 2 (i % 4) and the next.
+__device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Barrier over the softmax warps that also combines a predicate.
+__device__ __forceinline__ bool soft_bar_or(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(kSoftThreads)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+
+// Eight E2M1 codes of a word to four fp16 pairs, times the block's scale pair.
+__device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
+  uint32_t v[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&v[i]), s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// A key's raw bytes as one of its four lanes holds them: per part 32 codes
+// and two scales, and 16 rotary values.
+struct RawKey {
+  uint4 code[kParts];
+  uint16_t scale[kParts];
+  uint4 rope[2];
+};
+
+__device__ __forceinline__ void load_raw(RawKey& r, const AttendParams& p, int64_t slot, int part) {
+  if (slot >= 0) {
+    const uint8_t* e = p.kv + slot * kKvEntry;
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) {
+      r.code[s] = __ldg(reinterpret_cast<const uint4*>(e + s * 64 + part * 16));
+      r.scale[s] = __ldg(reinterpret_cast<const uint16_t*>(e + kKvScaleOff + s * 8 + part * 2));
+    }
+    r.rope[0] = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + part * 32));
+    r.rope[1] = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + part * 32 + 16));
+  } else {
+    // nothing listed: zeros, so that no bit pattern of the pool meets a zero weight
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) {
+      r.code[s] = make_uint4(0u, 0u, 0u, 0u);
+      r.scale[s] = 0;
+    }
+    r.rope[0] = r.rope[1] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
 
 // Pool row of list entry `pos` of sequence `seq`, or -1 (nothing listed, or a
 // position or page outside its range, which sets the status bit).
-__device__ __forceinline__ int64_t slot_of(const AttendParams& p, int seq, int pos) {
+__device__ __forceinline__ int64_t slot_of(const AttendParams& p, int seq, int pos, bool report) {
   if (pos < 0) return -1;
   const int blk = pos / p.page_size;
   if (blk < p.max_blocks) {
     const int page = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_blocks + blk);
     if (page >= 0 && page < p.n_pages) return static_cast<int64_t>(page) * p.page_size + (pos - blk * p.page_size);
   }
-  if (p.status) atomicOr(p.status, kErrOverflow);
+  if (report && p.status) atomicOr(p.status, kErrOverflow);
   return -1;
 }
 
-__global__ void __launch_bounds__(kAttThreads) attend_kv4_kernel(const AttendParams p) {
-  extern __shared__ float smem[];
-  float* s_k = smem;                              // [kAttKeys][kAttPitch]
-  float* s_q = s_k + kAttKeys * kAttPitch;        // [kAttHeads][kKvQ]
-  __shared__ int64_t s_slot[kAttKeys];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hb = (p.H + kAttHeads - 1) / kAttHeads;
-  const int64_t t = blockIdx.x / hb;
-  const int h = static_cast<int>(blockIdx.x % hb) * kAttHeads + warp;
+// Query rows to shared memory as the MMA reads them (see the file's comment),
+// row by row over `n_warps` warps.
+template <int NH>
+__device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
+                                              int warp, int n_warps, int lane) {
+  using L = AttSmem<NH>;
+  constexpr int kChunks = kKvQ / 8;  // 16-byte chunks of a row: 64 latent, 8 rotary
+  for (int r = warp; r < NH; r += n_warps) {
+    const bool live = h0 + r < p.H;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (t * p.H + h0 + r) * kKvQ);
+    uint4 v[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      v[i] = live && lane + 32 * i < kChunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      m = __vmaxu2(m, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+      m = __vmaxu2(m, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+    }
+    m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
+    const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (lane == 0) s_c[r] = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int c = lane + 32 * i;
+      if (c < kChunks) {
+        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
+          if (c < kKvLat / 8) {
+            const __half2 h = __floats2half2_rn(a, b);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        *reinterpret_cast<uint4*>(smem + (c >> 3) * L::q_block + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
+template <int NH>
+__global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const AttendParams p, const AttGrid g) {
+  using L = AttSmem<NH>;
+  constexpr uint32_t kTmemO = 0, kTmemS = kParts * NH;  // columns
+  constexpr uint32_t kTmemCols = (kParts + 2) * NH <= 128 ? 128u : (kParts + 2) * NH <= 256 ? 256u : 512u;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase, sK = sbase + L::off_k, sP = sbase + L::off_p;
+  float* s_c = reinterpret_cast<float*>(smem + L::off_c);
+  float* s_f = reinterpret_cast<float*>(smem + L::off_f);
+  volatile uint8_t* s_mask = smem + L::off_mask;
+  const uint32_t bars = sbase + L::off_bars;
+  auto bar_full = [&](int b, int s) { return bars + 8 * (b * kParts + s); };
+  auto bar_empty = [&](int b, int s) { return bars + 8 * (2 * kParts + b * kParts + s); };
+  auto bar_s = [&](int b) { return bars + 8 * (4 * kParts + b); };
+  const uint32_t bar_p = bars + 8 * (4 * kParts + 2), bar_o = bar_p + 8, bar_drain = bar_p + 16;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::off_misc);
+  int* s_last = reinterpret_cast<int*>(smem + L::off_misc + 4);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::off_misc + 8);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t item = blockIdx.x;
+  const int split = static_cast<int>(item % g.splits);
+  const int hb = static_cast<int>(item / g.splits % g.head_blocks);
+  const int64_t t = item / g.splits / g.head_blocks;
+  const int h0 = hb * NH;
   const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
-  if (seq < 0) return;
+  if (seq < 0) return;  // padding
   if (seq >= p.B) {
     if (tid == 0 && p.status) atomicOr(p.status, kErrOverflow);
     return;
   }
-  const bool live = h < p.H;
-  for (int d = lane; d < kKvQ; d += 32)
-    s_q[warp * kKvQ + d] = live ? __uint_as_float(static_cast<uint32_t>(p.q[(t * p.H + h) * kKvQ + d]) << 16) : 0.f;
-  float m = -INFINITY, sum = 0.f, acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < p.n; j0 += kAttKeys) {
-    __syncthreads();
-    if (tid < kAttKeys) s_slot[tid] = j0 + tid < p.n ? slot_of(p, seq, __ldg(p.idx + t * p.n + j0 + tid)) : -1;
-    __syncthreads();
-    for (int c = tid; c < kAttKeys * 32; c += kAttThreads) {  // one block of 16 dimensions
-      const int key = c >> 5, blk = c & 31;
-      const int64_t s = s_slot[key];
-      float* dst = s_k + key * kAttPitch + 16 * blk;
-      float* rdst = s_k + key * kAttPitch + kKvLat + 2 * blk;
-      if (s < 0) {
-        for (int i = 0; i < 16; ++i) dst[i] = 0.f;
-        rdst[0] = rdst[1] = 0.f;
-        continue;
-      }
-      const uint8_t* e = p.kv + s * kKvEntry;
-      const uint2 code = reinterpret_cast<const uint2*>(e)[blk];
-      const float sv = __half2float(__half(__nv_cvt_fp8_to_halfraw(e[kKvScaleOff + blk], __NV_E4M3)));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t by = ((i < 4 ? code.x : code.y) >> (8 * (i & 3))) & 0xFFu;
-        const float2 f =
-            __half22float2(__half2(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(by), __NV_E2M1)));
-        dst[2 * i] = f.x * sv;
-        dst[2 * i + 1] = f.y * sv;
-      }
-      const uint32_t r = reinterpret_cast<const uint32_t*>(e + kKvRopeOff)[blk];
-      rdst[0] = __uint_as_float(r << 16);
-      rdst[1] = __uint_as_float(r & 0xFFFF0000u);
+  const int j_lo = static_cast<int>(static_cast<int64_t>(g.tiles) * split / g.splits) * kKt;
+  const int j_hi = min(p.n, static_cast<int>(static_cast<int64_t>(g.tiles) * (split + 1) / g.splits) * kKt);
+  const int32_t* list = p.idx + t * p.n;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2 * kParts; ++i) {
+      mbar_init(bars + 8 * i, kLoadWarps);
+      mbar_init(bars + 8 * (2 * kParts + i), 1);
     }
-    __syncthreads();
-    const bool valid = s_slot[lane] >= 0;
-    float z = 0.f;
-    for (int d = 0; d < kKvQ; ++d) z = fmaf(s_q[warp * kKvQ + d], s_k[lane * kAttPitch + d], z);
-    z = valid ? z * p.scale : -INFINITY;
-    float mx = z;
+    mbar_init(bar_s(0), 1);
+    mbar_init(bar_s(1), 1);
+    mbar_init(bar_p, kSoftWarps);
+    mbar_init(bar_o, 1);
+    mbar_init(bar_drain, 1);
+    *s_last = -1;
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kSoftWarps + kLoadWarps) {
+    tmem_alloc(smem_u32(s_tmem), kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+
+  // the gathering lanes' place, and the first tile's loads
+  const int lw = warp - kSoftWarps, key = lw * 8 + (lane & 7), part = lane >> 3;
+  const bool loader = lw >= 0 && lw < kLoadWarps;
+  auto entry = [&](int tile) {
+    const int j = j_lo + tile * kKt + key;
+    return j < j_hi ? __ldg(list + j) : -1;
+  };
+  RawKey raw;
+  bool have = false;
+  int64_t slot1 = -1;
+  int pos2 = -1;
+  if (loader) {
+    const int64_t slot0 = slot_of(p, seq, entry(0), part == 0);
+    pos2 = entry(1);
+    load_raw(raw, p, slot0, part);
+    have = slot0 >= 0;
+    slot1 = slot_of(p, seq, pos2, part == 0);
+    pos2 = entry(2);
+  }
+  // tiles to run: up to the last entry that names a key
+  {
+    int last = -1;
+    for (int j = j_lo + tid; j < j_hi; j += kAttThreads)
+      if (__ldg(list + j) >= 0) last = j;
+    last = __reduce_max_sync(~0u, last);
+    if (lane == 0 && last >= 0) atomicMax(s_last, last);
+  }
+  if (warp < kSoftWarps + kLoadWarps) stage_queries<NH>(p, t, h0, smem, s_c, warp, kSoftWarps + kLoadWarps, lane);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int nt = *s_last < 0 ? 0 : (*s_last - j_lo) / kKt + 1;
+  const uint32_t tmem = *s_tmem;
+
+  if (loader) {
+    // ------------------------------------------------------------- gather
+    const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
+    for (int i = 0; i < nt; ++i) {
+      const int b = i & 1;
+      const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
+      RawKey next;
+      const bool have_next = slot1 >= 0;
+      load_raw(next, p, slot1, part);
+      slot1 = slot_of(p, seq, pos2, part == 0);
+      pos2 = entry(i + 3);
+      const uint32_t tile = sK + b * kTileBytes + row;
+      bool ok = true;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float f = __expf(m - ref), e = valid ? __expf(z - ref) : 0.f;
-    m = mn;
-    float es = e;
+      for (int s = 0; s < kParts; ++s) {
+        if (!(ok = __all_sync(~0u, mbar_wait(bar_empty(b, s), ph, s_abort, g.err)))) break;
+        if (s == 0) {
+          const uint32_t mask = __ballot_sync(~0u, have);
+          if (lane == 0) s_mask[b * 8 + lw] = static_cast<uint8_t>(mask);
+          const uint32_t dst = tile + 8 * kBlockBytes;
+          sts128(dst + (((2 * part) ^ sw) << 4), raw.rope[0].x, raw.rope[0].y, raw.rope[0].z, raw.rope[0].w);
+          sts128(dst + (((2 * part + 1) ^ sw) << 4), raw.rope[1].x, raw.rope[1].y, raw.rope[1].z, raw.rope[1].w);
+        }
+        const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(raw.scale[s], __NV_E4M3));
+        const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
+        const uint32_t dst = tile + (2 * s + (part >> 1)) * kBlockBytes;
+        const uint32_t w[4] = {raw.code[s].x, raw.code[s].y, raw.code[s].z, raw.code[s].w};
 #pragma unroll
-    for (int o = 16; o; o >>= 1) es += __shfl_xor_sync(~0u, es, o);
-    sum = sum * f + es;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] *= f;
-    for (int k = 0; k < kAttKeys; ++k) {
-      const float w = __shfl_sync(~0u, e, k);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[i] = fmaf(w, s_k[k * kAttPitch + i * 32 + lane], acc[i]);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
+          decode8(w[k], k < 2 ? lo : hi, o);
+          sts128(dst + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_full(b, s));
+      }
+      if (!ok) break;
+      raw = next;
+      have = have_next;
     }
-  }
-  if (!live) return;
-  const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+  } else if (warp == kSoftWarps + kLoadWarps) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0), kIdR = idesc_att(64, NH, 1, 0), kIdO = idesc_att(128, NH, 0, 1);
+      bool ok = true;
+      auto output = [&](int i) {  // O^T += V^T P^T of tile i
+        const int b = i & 1;
+        if (!mbar_wait(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
+        tc_fence_after();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(acc[i] * inv);
-    p.out[(t * p.H + h) * kKvLat + i * 32 + lane] = *reinterpret_cast<const uint16_t*>(&b);
+        for (int s = 0; s < kParts; ++s) {
+#pragma unroll
+          for (int k = 0; k < kKt / 16; ++k)
+            mma_bf16(tmem + kTmemO + s * NH, desc_mn_sw128(sK + b * kTileBytes + 2 * s * kBlockBytes + k * 2048, kBlockBytes),
+                     desc_mn_sw128(sP + k * 2048, kBlockBytes), kIdO, i > 0 || k > 0);
+          mma_commit(bar_empty(b, s));
+        }
+        mma_commit(bar_o);
+        return true;
+      };
+      for (int i = 0; i < nt && ok; ++i) {
+        const int b = i & 1;
+        const uint32_t d = tmem + kTmemS + b * NH;
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+          if (!(ok = mbar_wait(bar_full(b, s), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err))) break;
+          tc_fence_after();
+          if (s == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_bf16(d, smem_desc_sw128(sK + b * kTileBytes + 8 * kBlockBytes + 32 * k),
+                       smem_desc_sw128(sQ + 8 * L::q_block + 32 * k), kIdR, k > 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int blk = 2 * s + (k >> 2);
+            mma_bf16(d, smem_desc_sw128(sK + b * kTileBytes + blk * kBlockBytes + 32 * (k & 3)),
+                     smem_desc_sw128(sQ + blk * L::q_block + 32 * (k & 3)), kIdS, 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit(bar_s(b));
+        if (i > 0) ok = output(i - 1);
+      }
+      if (ok && nt > 0) output(nt - 1);
+      // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+      mma_commit(bar_drain);
+      int unused = 0;
+      mbar_wait(bar_drain, 0, &unused, g.err);
+    }
+    __syncwarp();
+  } else if (warp < kSoftWarps) {
+    // ------------------------------------------------------------ softmax
+    constexpr int C = NH / 4;  // columns per thread
+    float c[C], m[C], l[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      c[j] = s_c[(j >> 1) * 8 + 2 * (lane & 3) + (j & 1)];
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+    }
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t r0 = lane >> 2;
+    const uint32_t p0 = sP + (warp * 16 + r0) * 128 + (lane & 3) * 4;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      const int b = i & 1;
+      ok = __all_sync(~0u, mbar_wait(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;  // the mask
+      const bool v0 = (s_mask[b * 8 + 2 * warp] >> r0) & 1, v1 = (s_mask[b * 8 + 2 * warp + 1] >> r0) & 1;
+      ok = __all_sync(~0u, mbar_wait(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+      tc_fence_after();
+      uint32_t x[NH / 2];
+      tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, x);
+      tmem_wait_ld();
+      bool rise = !ok;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int k = 4 * (j >> 1) + (j & 1);
+        const float a = fmaf(__uint_as_float(x[k]), c[j], -m[j]), d = fmaf(__uint_as_float(x[k + 2]), c[j], -m[j]);
+        rise |= (v0 && a > kRise) || (v1 && d > kRise);
+      }
+      // the same decision in all four warps; a wait that gave up goes this way too
+      if (soft_bar_or(rise)) {
+        if (i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+        if (soft_bar_or(!ok)) break;
+        float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH]: P of the last tile is consumed
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const int k = 4 * (j >> 1) + (j & 1);
+          float mx = fmaxf(v0 ? __uint_as_float(x[k]) * c[j] : -INFINITY, v1 ? __uint_as_float(x[k + 2]) * c[j] : -INFINITY);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+          if (lane < 4) exch[warp * NH + (j >> 1) * 8 + 2 * lane + (j & 1)] = mx;
+        }
+        named_bar_sync(1, kSoftThreads);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const int col = (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
+          const float mn = fmaxf(fmaxf(fmaxf(exch[col], exch[NH + col]), fmaxf(exch[2 * NH + col], exch[3 * NH + col])), m[j]);
+          const float f = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
+          m[j] = mn;
+          l[j] *= f;
+          if (warp == 0 && lane < 4) s_f[col] = f;
+        }
+        named_bar_sync(1, kSoftThreads);
+        if (i > 0) {
+          for (int q = 0; q < kParts * NH; q += 16) {
+            uint32_t o[16];
+            tmem_ld16(tmem + kTmemO + lane_base + q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s_f[(q + k) % NH]);
+            tmem_st16(tmem + kTmemO + lane_base + q, o);
+          }
+          tmem_wait_st();
+        }
+      } else if (i > 0) {
+        ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+      }
+#pragma unroll
+      for (int j = 0; j < C; j += 2) {
+        const int k = 2 * j;
+        const float a0 = v0 ? ex2(fmaf(__uint_as_float(x[k]), c[j], -m[j])) : 0.f;
+        const float a1 = v0 ? ex2(fmaf(__uint_as_float(x[k + 1]), c[j + 1], -m[j + 1])) : 0.f;
+        const float d0 = v1 ? ex2(fmaf(__uint_as_float(x[k + 2]), c[j], -m[j])) : 0.f;
+        const float d1 = v1 ? ex2(fmaf(__uint_as_float(x[k + 3]), c[j + 1], -m[j + 1])) : 0.f;
+        l[j] += a0 + d0;
+        l[j + 1] += a1 + d1;
+        const __half2 ha = __floats2half2_rn(a0, a1), hd = __floats2half2_rn(d0, d1);
+        const uint32_t at = p0 + (((j >> 1) ^ r0) << 4);
+        sts32(at, *reinterpret_cast<const uint32_t*>(&ha));
+        sts32(at + 8 * 128, *reinterpret_cast<const uint32_t*>(&hd));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p);
+    }
+    // ------------------------------------------------------------- output
+    if (nt > 0) mbar_wait(bar_o, static_cast<uint32_t>(nt - 1) & 1u, s_abort, g.err);
+    __syncwarp();
+    tc_fence_after();
+    float* exch = reinterpret_cast<float*>(smem + L::off_p);
+    named_bar_sync(1, kSoftThreads);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], o);
+      if (lane < 4) exch[warp * NH + (j >> 1) * 8 + 2 * lane + (j & 1)] = l[j];
+    }
+    named_bar_sync(1, kSoftThreads);
+    if (warp == 0 && lane < 4) {
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int col = (j >> 1) * 8 + 2 * lane + (j & 1);
+        const float sum = (exch[col] + exch[NH + col]) + (exch[2 * NH + col] + exch[3 * NH + col]);
+        if (g.splits > 1) {
+          g.part_ml[item * NH + col] = make_float2(m[j], sum);
+          s_f[col] = 1.f;
+        } else {
+          s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
+          if (p.lse && h0 + col < p.H)
+            p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (m[j] + log2f(sum)) * 0.69314718055994531f;
+        }
+      }
+    }
+    named_bar_sync(1, kSoftThreads);
+    for (int s = 0; s < kParts; ++s) {
+      const int dim = s * 128 + warp * 32 + lane;
+      for (int q = 0; q < NH; q += 16) {
+        if (h0 + q >= p.H) break;
+        uint32_t o[16];
+        if (nt > 0) {
+          tmem_ld16(tmem + kTmemO + s * NH + lane_base + q, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = 0u;
+        }
+        if (g.splits > 1) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            if (h0 + q + k < p.H) g.part_o[(item * NH + q + k) * kKvLat + dim] = __uint_as_float(o[k]);
+        } else {
+          // lanes pair up: the even one stores two dimensions of head q + k, the odd one of q + k + 1
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float a = __uint_as_float(o[k]) * s_f[q + k], b = __uint_as_float(o[k + 1]) * s_f[q + k + 1];
+            const float other = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
+            const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
+            const int h = h0 + q + k + (lane & 1);
+            if (h < p.H)
+              *reinterpret_cast<__nv_bfloat162*>(p.out + (t * p.H + h) * kKvLat + (dim & ~1)) = v;
+          }
+        }
+      }
+    }
+    tc_fence_before();
   }
-  if (p.lse && lane == 0) p.lse[t * p.H + h] = m + logf(sum);
+  __syncthreads();
+  if (warp == kSoftWarps + kLoadWarps) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the splits of one (row, head): out = sum_s 2^(m_s - m) O_s / sum_s
+// 2^(m_s - m) l_s.
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p, const AttGrid g, int NH) {
+  const int64_t t = blockIdx.x / p.H;
+  const int h = static_cast<int>(blockIdx.x % p.H);
+  const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
+  if (seq < 0 || seq >= p.B) return;
+  const int64_t item0 = (t * g.head_blocks + h / NH) * g.splits;
+  const int col = h % NH;
+  float m = -INFINITY;
+  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.part_ml[(item0 + s) * NH + col].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < g.splits; ++s) {
+    const float2 ml = g.part_ml[(item0 + s) * NH + col];
+    const float w = ex2(ml.x - ref);
+    const float4 o = reinterpret_cast<const float4*>(g.part_o + ((item0 + s) * NH + col) * kKvLat)[threadIdx.x];
+    sum = fmaf(w, ml.y, sum);
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kKvLat)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (p.lse && threadIdx.x == 0)
+    p.lse[t * p.H + h] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
+struct AttPlan {
+  int NH, head_blocks, splits, tiles;
+  size_t off_ml, off_o, bytes;
+};
+
+AttPlan plan_attend(int64_t T, int H, int n, int sms) {
+  AttPlan P{};
+  P.NH = H <= 16 ? 16 : H <= 32 ? 32 : 64;
+  P.head_blocks = (H + P.NH - 1) / P.NH;
+  P.tiles = (n + kKt - 1) / kKt;
+  const int64_t items = T * P.head_blocks;
+  P.splits = items >= sms || items == 0 ? 1 : static_cast<int>(std::min<int64_t>(sms / items, P.tiles));
+  P.off_ml = 256;
+  P.off_o = P.off_ml;
+  P.bytes = 256;
+  if (P.splits > 1) {
+    const size_t rows = static_cast<size_t>(items) * P.splits * P.NH;
+    P.off_o = (P.off_ml + rows * sizeof(float2) + 255) / 256 * 256;
+    P.bytes = P.off_o + rows * kKvLat * sizeof(float);
+  }
+  return P;
+}
+
+template <int NH>
+cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, cudaStream_t st) {
+  constexpr int bytes = AttSmem<NH>::request;
+  cudaError_t e = cudaFuncSetAttribute(attend_kv4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = p.T * g.head_blocks * g.splits;
+  attend_kv4_kernel<NH><<<static_cast<unsigned>(grid), kAttThreads, bytes, st>>>(p, g);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attend_kv4(const AttendParams& p, int sms, cudaStream_t st) {
-  (void)sms;
-  constexpr int bytes = (kAttKeys * kAttPitch + kAttHeads * kKvQ) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attend_kv4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = p.T * ((p.H + kAttHeads - 1) / kAttHeads);
-  attend_kv4_kernel<<<static_cast<unsigned>(grid), kAttThreads, bytes, st>>>(p);
+size_t attend_workspace_bytes(int64_t T, int H, int n, int sms) { return plan_attend(T, H, n, sms).bytes; }
+
+cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st) {
+  const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float*>(ws + P.off_o),
+            reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
+  cudaError_t e = P.NH == 16 ? launch_nh<16>(p, g, st) : P.NH == 32 ? launch_nh<32>(p, g, st) : launch_nh<64>(p, g, st);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  attend_join_kernel<<<static_cast<unsigned>(p.T * p.H), 128, 0, st>>>(p, g, P.NH);
   return cudaGetLastError();
 }
 

@@ -102,6 +102,7 @@ struct AttendParams {
   float* lse;                  // [T][H] or null
   uint32_t* status;            // may be null
 };
-cudaError_t launch_attend_kv4(const AttendParams& p, int sms, cudaStream_t st);
+size_t attend_workspace_bytes(int64_t T, int H, int n, int sms);
+cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st);
 
 }  // namespace dsa

@@ -79,7 +79,7 @@ def attend(L, q=d, kv=d, n_pages=8, page=64, table=d, B=2, blocks=4, seq=d, idx=
 def test_attend_refusals():
     L = dsa.lib()
     assert attend(L, H=0) == -2 and attend(L, H=257) == -2
-    assert attend(L, n=0) == -1 and attend(L, T=-1) == -1 and attend(L, T=1 << 31, need=1 << 40) == -1
+    assert attend(L, n=0) == -1 and attend(L, n=(1 << 30) + 1, need=1 << 40) == -1 and attend(L, T=-1) == -1 and attend(L, T=1 << 31, need=1 << 40) == -1
     assert attend(L, page=0) == -1 and attend(L, n_pages=1 << 31) == -1 and attend(L, blocks=1 << 28) == -1
     assert attend(L, scale=float("inf")) == -1 and attend(L, scale=float("nan")) == -1
     assert attend(L, B=0) == -1 and attend(L, seq=None, T=3) == -1
