@@ -22,6 +22,13 @@
 //               tile ahead into registers, E2M1 -> fp16 times the block scale
 //               (exact), and store the swizzled tile, two tile buffers
 //   warp 12     issues the MMAs
+//   warp 13     reads the list and the block table and packs the pool rows of
+//               the entries that name a key into tiles, so that gaps and
+//               short lists cost no tiles
+//
+// A lane decodes 128 consecutive dimensions of its key, 32 per hand-over part
+// (below), so position 128 s + 32 p + r of a decoded tile is latent dimension
+// 128 p + 32 s + r; the staged queries and the output rows are in that order.
 //
 // A tile buffer is handed over in four parts of 128 dimensions, both ways:
 // O^T's product over a part frees it, so the next tile's decoding and scores
@@ -59,7 +66,9 @@ constexpr int kParts = kKvLat / 128;             // hand-over parts of a tile bu
 constexpr uint32_t kBlockBytes = kKt * 128;      // one column block
 constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
 constexpr int kSoftWarps = 4, kLoadWarps = 8;
-constexpr int kAttThreads = (kSoftWarps + kLoadWarps + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1;
+constexpr int kAttThreads = (kListWarp + 1) * 32;
+constexpr int kRing = 4;                         // tiles of slots that the list warp may be ahead
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr float kRise = 8.f;                     // log2 of the largest P before the reference moves
 constexpr float kLog2e = 1.4426950408889634f;
@@ -71,13 +80,15 @@ struct AttSmem {
   static constexpr uint32_t off_p = off_k + 2 * kTileBytes;
   static constexpr uint32_t off_c = off_p + kKt * 128;   // per head: factor of a score in log2 units
   static constexpr uint32_t off_f = off_c + NH * 4;      // per head: rescaling factor, then 1 / sum
-  static constexpr uint32_t off_mask = off_f + NH * 4;   // per tile buffer: one bit per key
-  static constexpr uint32_t off_bars = off_mask + 16;
-  // part full and empty [2 buffers][4], scores [2], weights, output, drain
-  static constexpr uint32_t n_bars = 4 * kParts + 2 + 3;
+  static constexpr uint32_t off_ring = off_f + NH * 4;   // pool rows of the next tiles' keys
+  static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // keys of each ring tile, then of each buffer
+  static constexpr uint32_t off_bars = off_count + (kRing + 2) * 4;
+  // part full and empty [2 buffers][4], ring full and empty, scores [2], weights, output, drain
+  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 2 + 3;
   static constexpr uint32_t off_misc = off_bars + 8 * n_bars;
   static constexpr uint32_t bytes = off_misc + 16;
   static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
+  static_assert(off_bars % 8 == 0, "mbarrier alignment");
 };
 static_assert(AttSmem<64>::request <= 227u * 1024u, "shared memory budget");
 
@@ -187,45 +198,53 @@ __device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t (&o)[4])
   }
 }
 
-// A key's raw bytes as one of its four lanes holds them: per part 32 codes
-// and two scales, and 16 rotary values.
+// A key's raw bytes as one of its four lanes holds them: 128 codes, their
+// eight scales and 16 rotary values.
 struct RawKey {
-  uint4 code[kParts];
-  uint16_t scale[kParts];
-  uint4 rope[2];
+  uint32_t code[16];
+  uint2 scale;
+  uint32_t rope[8];
 };
 
-__device__ __forceinline__ void load_raw(RawKey& r, const AttendParams& p, int64_t slot, int part) {
-  if (slot >= 0) {
-    const uint8_t* e = p.kv + slot * kKvEntry;
+__device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
+  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "l"(p));
+}
+
+__device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot, bool live, int part) {
+  if (live) {
+    const uint8_t* e = kv + static_cast<int64_t>(slot) * kKvEntry;
+    uint32_t a[8], b[8];
+    ldg256(a, e + part * 64);
+    ldg256(b, e + part * 64 + 32);
+    r.scale = __ldg(reinterpret_cast<const uint2*>(e + kKvScaleOff + part * 8));
+    ldg256(r.rope, e + kKvRopeOff + part * 32);
 #pragma unroll
-    for (int s = 0; s < kParts; ++s) {
-      r.code[s] = __ldg(reinterpret_cast<const uint4*>(e + s * 64 + part * 16));
-      r.scale[s] = __ldg(reinterpret_cast<const uint16_t*>(e + kKvScaleOff + s * 8 + part * 2));
+    for (int i = 0; i < 8; ++i) {
+      r.code[i] = a[i];
+      r.code[8 + i] = b[i];
     }
-    r.rope[0] = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + part * 32));
-    r.rope[1] = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + part * 32 + 16));
   } else {
-    // nothing listed: zeros, so that no bit pattern of the pool meets a zero weight
+    // behind the last key: zeros, so that no bit pattern of the pool meets a zero weight
 #pragma unroll
-    for (int s = 0; s < kParts; ++s) {
-      r.code[s] = make_uint4(0u, 0u, 0u, 0u);
-      r.scale[s] = 0;
-    }
-    r.rope[0] = r.rope[1] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 16; ++i) r.code[i] = 0u;
+    r.scale = make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.rope[i] = 0u;
   }
 }
 
 // Pool row of list entry `pos` of sequence `seq`, or -1 (nothing listed, or a
-// position or page outside its range, which sets the status bit).
-__device__ __forceinline__ int64_t slot_of(const AttendParams& p, int seq, int pos, bool report) {
+// position or page outside its range, which sets `bad`).
+__device__ __forceinline__ int slot_of(const AttendParams& p, const int32_t* table, int pos, bool& bad) {
   if (pos < 0) return -1;
-  const int blk = pos / p.page_size;
+  const int blk = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
   if (blk < p.max_blocks) {
-    const int page = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_blocks + blk);
-    if (page >= 0 && page < p.n_pages) return static_cast<int64_t>(page) * p.page_size + (pos - blk * p.page_size);
+    const int page = __ldg(table + blk);
+    if (page >= 0 && page < p.n_pages) return page * p.page_size + (pos - blk * p.page_size);
   }
-  if (report && p.status) atomicOr(p.status, kErrOverflow);
+  bad = true;
   return -1;
 }
 
@@ -270,7 +289,10 @@ __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, 
             o[k] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
-        *reinterpret_cast<uint4*>(smem + (c >> 3) * L::q_block + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+        // column block and 16-byte chunk of latent dimensions 8 c .. 8 c + 7 (the order of the decoded tiles)
+        const int blk = c < kKvLat / 8 ? ((c >> 1) & 6) + (c >> 5) : 8;
+        const int at = c < kKvLat / 8 ? ((c >> 2) & 4) + (c & 3) : c & 7;
+        *reinterpret_cast<uint4*>(smem + blk * L::q_block + r * 128 + ((at ^ (r & 7)) << 4)) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
@@ -289,14 +311,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   const uint32_t sQ = sbase, sK = sbase + L::off_k, sP = sbase + L::off_p;
   float* s_c = reinterpret_cast<float*>(smem + L::off_c);
   float* s_f = reinterpret_cast<float*>(smem + L::off_f);
-  volatile uint8_t* s_mask = smem + L::off_mask;
+  volatile int* s_ring = reinterpret_cast<volatile int*>(smem + L::off_ring);
+  volatile int* s_ring_n = reinterpret_cast<volatile int*>(smem + L::off_count);
+  volatile int* s_n = s_ring_n + kRing;
   const uint32_t bars = sbase + L::off_bars;
   auto bar_full = [&](int b, int s) { return bars + 8 * (b * kParts + s); };
   auto bar_empty = [&](int b, int s) { return bars + 8 * (2 * kParts + b * kParts + s); };
-  auto bar_s = [&](int b) { return bars + 8 * (4 * kParts + b); };
-  const uint32_t bar_p = bars + 8 * (4 * kParts + 2), bar_o = bar_p + 8, bar_drain = bar_p + 16;
+  auto bar_listed = [&](int r) { return bars + 8 * (4 * kParts + r); };
+  auto bar_taken = [&](int r) { return bars + 8 * (4 * kParts + kRing + r); };
+  auto bar_s = [&](int b) { return bars + 8 * (4 * kParts + 2 * kRing + b); };
+  const uint32_t bar_p = bar_s(2), bar_o = bar_p + 8, bar_drain = bar_p + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::off_misc);
-  int* s_last = reinterpret_cast<int*>(smem + L::off_misc + 4);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::off_misc + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -325,96 +350,134 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     mbar_init(bar_p, kSoftWarps);
     mbar_init(bar_o, 1);
     mbar_init(bar_drain, 1);
-    *s_last = -1;
+    for (int r = 0; r < kRing; ++r) {
+      mbar_init(bar_listed(r), 1);
+      mbar_init(bar_taken(r), kLoadWarps);
+    }
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (warp == kSoftWarps + kLoadWarps) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tmem_relinquish();
   }
   __syncthreads();
 
-  // the gathering lanes' place, and the first tile's loads
   const int lw = warp - kSoftWarps, key = lw * 8 + (lane & 7), part = lane >> 3;
-  const bool loader = lw >= 0 && lw < kLoadWarps;
-  auto entry = [&](int tile) {
-    const int j = j_lo + tile * kKt + key;
-    return j < j_hi ? __ldg(list + j) : -1;
-  };
-  RawKey raw;
-  bool have = false;
-  int64_t slot1 = -1;
-  int pos2 = -1;
-  if (loader) {
-    const int64_t slot0 = slot_of(p, seq, entry(0), part == 0);
-    pos2 = entry(1);
-    load_raw(raw, p, slot0, part);
-    have = slot0 >= 0;
-    slot1 = slot_of(p, seq, pos2, part == 0);
-    pos2 = entry(2);
+  if (warp < kMmaWarp) {
+    stage_queries<NH>(p, t, h0, smem, s_c, warp, kMmaWarp, lane);
+    fence_proxy_async_smem();
+    tc_fence_before();
+    named_bar_sync(2, (kMmaWarp + 1) * 32);
+    tc_fence_after();
   }
-  // tiles to run: up to the last entry that names a key
-  {
-    int last = -1;
-    for (int j = j_lo + tid; j < j_hi; j += kAttThreads)
-      if (__ldg(list + j) >= 0) last = j;
-    last = __reduce_max_sync(~0u, last);
-    if (lane == 0 && last >= 0) atomicMax(s_last, last);
-  }
-  if (warp < kSoftWarps + kLoadWarps) stage_queries<NH>(p, t, h0, smem, s_c, warp, kSoftWarps + kLoadWarps, lane);
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const int nt = *s_last < 0 ? 0 : (*s_last - j_lo) / kKt + 1;
-  const uint32_t tmem = *s_tmem;
-
-  if (loader) {
+  if (warp == kListWarp) {
+    // --------------------------------------------------------------- list
+    // Packs the pool rows of the entries that name a key into tiles, ahead of
+    // the gathering warps; a tile of 0 keys ends the list.
+    const int32_t* table = p.block_table + static_cast<int64_t>(seq) * p.max_blocks;
+    int total = 0;  // keys packed; total / kKt tiles are published
+    bool ok = true, bad = false;
+    auto open_tile = [&](int tile) {  // before the first write to a ring tile
+      return __all_sync(~0u, mbar_wait(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
+    };
+    auto publish = [&](int tile, int count) {
+      if (lane == 0) s_ring_n[tile % kRing] = count;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
+    };
+    int pos[4];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
+    };
+    fetch(j_lo);
+    for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
+      int slot[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) slot[k] = slot_of(p, table, pos[k], bad);
+      fetch(j0 + 128);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
+        const int cnt = __popc(m), at = total + __popc(m & lanemask_lt()), end = total + cnt;
+        if (cnt == 0) continue;
+        // a tile is opened by the batch that writes its first key
+        const int first = (total + kKt - 1) / kKt, last = (end - 1) / kKt;
+        if (last >= first && !(ok = open_tile(last))) break;
+        if (slot[k] >= 0) s_ring[at % (kRing * kKt)] = slot[k];
+        __syncwarp();
+        if (end / kKt > total / kKt) publish(total / kKt, kKt);
+        total = end;
+      }
+    }
+    if (ok && total % kKt) {
+      publish(total / kKt, total % kKt);
+      total += kKt - total % kKt;
+    }
+    if (ok && open_tile(total / kKt)) publish(total / kKt, 0);
+    if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
+  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
     // ------------------------------------------------------------- gather
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
-    for (int i = 0; i < nt; ++i) {
+    RawKey raw;
+    int n_keys = 0;
+    bool ok = true;
+    auto take = [&](RawKey& r, int& count, int tile) {  // a tile's loads, once its slots are listed
+      const int k = tile % kRing;
+      if (!__all_sync(~0u, mbar_wait(bar_listed(k), static_cast<uint32_t>(tile / kRing) & 1u, s_abort, g.err))) return false;
+      count = s_ring_n[k];
+      load_raw(r, p.kv, s_ring[k * kKt + key], key < count, part);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_taken(k));
+      return true;
+    };
+    ok = take(raw, n_keys, 0);
+    for (int i = 0; ok; ++i) {
       const int b = i & 1;
       const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
       RawKey next;
-      const bool have_next = slot1 >= 0;
-      load_raw(next, p, slot1, part);
-      slot1 = slot_of(p, seq, pos2, part == 0);
-      pos2 = entry(i + 3);
+      int n_next = 0;
+      if (n_keys > 0 && !(ok = take(next, n_next, i + 1))) break;
       const uint32_t tile = sK + b * kTileBytes + row;
-      bool ok = true;
 #pragma unroll
       for (int s = 0; s < kParts; ++s) {
         if (!(ok = __all_sync(~0u, mbar_wait(bar_empty(b, s), ph, s_abort, g.err)))) break;
         if (s == 0) {
-          const uint32_t mask = __ballot_sync(~0u, have);
-          if (lane == 0) s_mask[b * 8 + lw] = static_cast<uint8_t>(mask);
+          if (lw == 0 && lane == 0) s_n[b] = n_keys;
           const uint32_t dst = tile + 8 * kBlockBytes;
-          sts128(dst + (((2 * part) ^ sw) << 4), raw.rope[0].x, raw.rope[0].y, raw.rope[0].z, raw.rope[0].w);
-          sts128(dst + (((2 * part + 1) ^ sw) << 4), raw.rope[1].x, raw.rope[1].y, raw.rope[1].z, raw.rope[1].w);
+          sts128(dst + (((2 * part) ^ sw) << 4), raw.rope[0], raw.rope[1], raw.rope[2], raw.rope[3]);
+          sts128(dst + (((2 * part + 1) ^ sw) << 4), raw.rope[4], raw.rope[5], raw.rope[6], raw.rope[7]);
         }
-        const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(raw.scale[s], __NV_E4M3));
+        const uint32_t sw2 = (s < 2 ? raw.scale.x : raw.scale.y) >> (16 * (s & 1));
+        const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(sw2 & 0xFFFFu), __NV_E4M3));
         const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
         const uint32_t dst = tile + (2 * s + (part >> 1)) * kBlockBytes;
-        const uint32_t w[4] = {raw.code[s].x, raw.code[s].y, raw.code[s].z, raw.code[s].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t o[4];
-          decode8(w[k], k < 2 ? lo : hi, o);
+          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
           sts128(dst + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_full(b, s));
+        if (n_keys == 0) break;  // the end of the list: part 0 alone carries it
       }
-      if (!ok) break;
+      if (!ok || n_keys == 0) break;
       raw = next;
-      have = have_next;
+      n_keys = n_next;
     }
-  } else if (warp == kSoftWarps + kLoadWarps) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
+    named_bar_sync(2, (kMmaWarp + 1) * 32);
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    if (elect_one()) {
       constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0), kIdR = idesc_att(64, NH, 1, 0), kIdO = idesc_att(128, NH, 0, 1);
+      // descriptors advance by their 16-byte address field
+      const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ), dV = desc_mn_sw128(sK, kBlockBytes),
+                     dP = desc_mn_sw128(sP, kBlockBytes);
       bool ok = true;
       auto output = [&](int i) {  // O^T += V^T P^T of tile i
         const int b = i & 1;
@@ -424,38 +487,40 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         for (int s = 0; s < kParts; ++s) {
 #pragma unroll
           for (int k = 0; k < kKt / 16; ++k)
-            mma_bf16(tmem + kTmemO + s * NH, desc_mn_sw128(sK + b * kTileBytes + 2 * s * kBlockBytes + k * 2048, kBlockBytes),
-                     desc_mn_sw128(sP + k * 2048, kBlockBytes), kIdO, i > 0 || k > 0);
+            mma_bf16(tmem + kTmemO + s * NH, dV + ((b * kTileBytes + 2 * s * kBlockBytes + k * 2048) >> 4),
+                     dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
           mma_commit(bar_empty(b, s));
         }
         mma_commit(bar_o);
         return true;
       };
-      for (int i = 0; i < nt && ok; ++i) {
+      int i = 0;
+      for (; ok; ++i) {
         const int b = i & 1;
-        const uint32_t d = tmem + kTmemS + b * NH;
+        const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
+        if (!(ok = mbar_wait(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
 #pragma unroll
         for (int s = 0; s < kParts; ++s) {
-          if (!(ok = mbar_wait(bar_full(b, s), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err))) break;
+          if (s > 0 && !(ok = mbar_wait(bar_full(b, s), ph, s_abort, g.err))) break;
           tc_fence_after();
           if (s == 0) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              mma_bf16(d, smem_desc_sw128(sK + b * kTileBytes + 8 * kBlockBytes + 32 * k),
-                       smem_desc_sw128(sQ + 8 * L::q_block + 32 * k), kIdR, k > 0);
+              mma_bf16(d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4), dQ + ((8 * L::q_block + 32 * k) >> 4),
+                       kIdR, k > 0);
           }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int blk = 2 * s + (k >> 2);
-            mma_bf16(d, smem_desc_sw128(sK + b * kTileBytes + blk * kBlockBytes + 32 * (k & 3)),
-                     smem_desc_sw128(sQ + blk * L::q_block + 32 * (k & 3)), kIdS, 1);
+            mma_bf16(d, dK + ((b * kTileBytes + blk * kBlockBytes + 32 * (k & 3)) >> 4),
+                     dQ + ((blk * L::q_block + 32 * (k & 3)) >> 4), kIdS, 1);
           }
         }
         if (!ok) break;
         mma_commit(bar_s(b));
         if (i > 0) ok = output(i - 1);
       }
-      if (ok && nt > 0) output(nt - 1);
+      if (ok && i > 0) output(i - 1);
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
       mma_commit(bar_drain);
       int unused = 0;
@@ -475,27 +540,34 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t r0 = lane >> 2;
     const uint32_t p0 = sP + (warp * 16 + r0) * 128 + (lane & 3) * 4;
+    const uint32_t tmem = *s_tmem;
     bool ok = true;
-    for (int i = 0; i < nt; ++i) {
+    int nt = 0;  // tiles
+    for (int i = 0;; nt = ++i) {
       const int b = i & 1;
-      ok = __all_sync(~0u, mbar_wait(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;  // the mask
-      const bool v0 = (s_mask[b * 8 + 2 * warp] >> r0) & 1, v1 = (s_mask[b * 8 + 2 * warp + 1] >> r0) & 1;
-      ok = __all_sync(~0u, mbar_wait(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+      ok = __all_sync(~0u, mbar_wait(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+      const int n_keys = ok ? s_n[b] : 0;
+      const bool v0 = warp * 16 + static_cast<int>(r0) < n_keys, v1 = warp * 16 + 8 + static_cast<int>(r0) < n_keys;
+      if (n_keys > 0)
+        ok = __all_sync(~0u, mbar_wait(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+      const bool end = !ok || n_keys == 0;
       tc_fence_after();
       uint32_t x[NH / 2];
-      tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, x);
-      tmem_wait_ld();
-      bool rise = !ok;
+      if (n_keys > 0) {
+        tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, x);
+        tmem_wait_ld();
+      }
+      bool rise = end;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         const int k = 4 * (j >> 1) + (j & 1);
         const float a = fmaf(__uint_as_float(x[k]), c[j], -m[j]), d = fmaf(__uint_as_float(x[k + 2]), c[j], -m[j]);
         rise |= (v0 && a > kRise) || (v1 && d > kRise);
       }
-      // the same decision in all four warps; a wait that gave up goes this way too
+      // the same decision in all four warps; the end of the list and a wait that gave up go this way too
       if (soft_bar_or(rise)) {
         if (i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
-        if (soft_bar_or(!ok)) break;
+        if (soft_bar_or(end || !ok)) break;
         float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH]: P of the last tile is consumed
 #pragma unroll
         for (int j = 0; j < C; ++j) {
@@ -579,7 +651,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     }
     named_bar_sync(1, kSoftThreads);
     for (int s = 0; s < kParts; ++s) {
-      const int dim = s * 128 + warp * 32 + lane;
+      const int dim = warp * 128 + s * 32 + lane;
       for (int q = 0; q < NH; q += 16) {
         if (h0 + q >= p.H) break;
         uint32_t o[16];
@@ -611,9 +683,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kSoftWarps + kLoadWarps) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(*s_tmem, kTmemCols);
   }
 }
 
