@@ -17,22 +17,22 @@
 // blocks of [64 keys][128 bytes] with the 128-byte swizzle, read K-major for
 // S and M-major for O.
 //
-//   warps 0-3   softmax and output: S^T from TMEM, exp2, P^T to shared memory
-//   warps 4-11  gather and decode: four lanes per key load its 416 bytes one
-//               tile ahead into registers, E2M1 -> fp16 times the block scale
-//               (exact), and store the swizzled tile, two tile buffers
-//   warp 12     issues the MMAs
-//   warp 13     reads the list and the block table and packs the pool rows of
-//               the entries that name a key into tiles, so that gaps and
-//               short lists cost no tiles
-//
-// A lane decodes 128 consecutive dimensions of its key, 32 per hand-over part
-// (below), so position 128 s + 32 p + r of a decoded tile is latent dimension
-// 128 p + 32 s + r; the staged queries and the output rows are in that order.
+//   warps 0-3    softmax: S^T from TMEM, exp2, P^T to shared memory
+//   warps 4-19   gather and decode: eight lanes per key load its 416 bytes one
+//                tile ahead into registers, E2M1 -> fp16 times the block scale
+//                (exact), and store the swizzled tile, two tile buffers; at
+//                the end O^T from TMEM through shared memory to the output
+//   warp 20      issues the MMAs
+//   warp 21      reads the list and the block table and packs the pool rows of
+//                the entries that name a key into tiles, so that gaps and
+//                short lists cost no tiles
 //
 // A tile buffer is handed over in four parts of 128 dimensions, both ways:
 // O^T's product over a part frees it, so the next tile's decoding and scores
-// follow part by part.
+// follow part by part.  The gathering warps are two groups of eight; each
+// lane decodes 64 consecutive dimensions of its key, 32 for each of its
+// group's two parts (part_dim gives the order; staged queries and output rows
+// follow it).
 //
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
 // bits, 2^-10 .. 2688).  Queries go to fp16 too, each row scaled by the power
@@ -65,12 +65,17 @@ constexpr int kBlocks = kKvQ / 64;               // 64-dimension column blocks: 
 constexpr int kParts = kKvLat / 128;             // hand-over parts of a tile buffer
 constexpr uint32_t kBlockBytes = kKt * 128;      // one column block
 constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
-constexpr int kSoftWarps = 4, kLoadWarps = 8;
+constexpr int kSoftWarps = 4, kLoadWarps = 16;   // loaders: two groups of 8 warps, 8 keys a warp
 constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1;
-constexpr int kAttThreads = (kListWarp + 1) * 32;
+constexpr int kAttThreads = (kListWarp + 3) * 32;     // whole warpgroups: two warps of the last one idle
+constexpr int kWorkThreads = (kSoftWarps + kLoadWarps) * 32;
+// registers per thread: 80 at launch, then shared out by warpgroup
+constexpr uint32_t kSoftRegs = 136, kLoadRegs = 72, kIssueRegs = 56;
+static_assert(kSoftRegs * 128 + kLoadRegs * 512 + kIssueRegs * 128 <= 80 * kAttThreads, "register pool");
 constexpr int kRing = 4;                         // tiles of slots that the list warp may be ahead
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr float kRise = 8.f;                     // log2 of the largest P before the reference moves
+constexpr uint32_t kOutRow = 2 * kKvLat + 16;     // staged output row, padded against bank conflicts
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NH>
@@ -89,13 +94,14 @@ struct AttSmem {
   static constexpr uint32_t bytes = off_misc + 16;
   static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
   static_assert(off_bars % 8 == 0, "mbarrier alignment");
+  static_assert(NH * kOutRow <= 2 * kTileBytes, "output staging");
 };
 static_assert(AttSmem<64>::request <= 227u * 1024u, "shared memory budget");
 
 // One row, head block and list range of the grid.
 struct AttGrid {
   int head_blocks, splits, tiles;  // tiles: of a whole list
-  float* part_o;                   // [T][head_blocks][splits][NH][512]
+  float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
   float2* part_ml;                 // [T][head_blocks][splits][NH]
   uint32_t* err;
 };
@@ -176,6 +182,20 @@ __device__ __forceinline__ bool soft_bar_or(bool v) {
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// Four 8 x 8 matrices of 16-bit fragments, transposed: lane 8 i + r gives the
+// address of column r of matrix i.
+__device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+// Bulk copy shared -> global (16-byte aligned, whole 16 bytes) and the wait until this thread's copies have read it.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
@@ -198,12 +218,12 @@ __device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t (&o)[4])
   }
 }
 
-// A key's raw bytes as one of its four lanes holds them: 128 codes, their
-// eight scales and 16 rotary values.
+// A key's raw bytes as one of its eight lanes (two groups of four) holds them:
+// 64 codes, their four scales and 8 rotary values.
 struct RawKey {
-  uint32_t code[16];
-  uint2 scale;
-  uint32_t rope[8];
+  uint32_t code[8];
+  uint32_t scale;
+  uint4 rope;
 };
 
 __device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
@@ -212,28 +232,24 @@ __device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
       : "l"(p));
 }
 
-__device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot, bool live, int part) {
+__device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot, bool live, int part, int group) {
   if (live) {
     const uint8_t* e = kv + static_cast<int64_t>(slot) * kKvEntry;
-    uint32_t a[8], b[8];
-    ldg256(a, e + part * 64);
-    ldg256(b, e + part * 64 + 32);
-    r.scale = __ldg(reinterpret_cast<const uint2*>(e + kKvScaleOff + part * 8));
-    ldg256(r.rope, e + kKvRopeOff + part * 32);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      r.code[i] = a[i];
-      r.code[8 + i] = b[i];
-    }
+    ldg256(r.code, e + part * 64 + group * 32);
+    r.scale = __ldg(reinterpret_cast<const uint32_t*>(e + kKvScaleOff + part * 8 + group * 4));
+    r.rope = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + (2 * part + group) * 16));
   } else {
     // behind the last key: zeros, so that no bit pattern of the pool meets a zero weight
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r.code[i] = 0u;
-    r.scale = make_uint2(0u, 0u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.rope[i] = 0u;
+    for (int i = 0; i < 8; ++i) r.code[i] = 0u;
+    r.scale = 0u;
+    r.rope = make_uint4(0u, 0u, 0u, 0u);
   }
 }
+
+// Hand-over part s of a tile and its latent dimensions: position 128 s + 32 p
+// + r holds dimension 128 p + 32 part_dim(s) + r (the map is its own inverse).
+__device__ __forceinline__ constexpr int part_dim(int s) { return 2 * (s & 1) + (s >> 1); }
 
 // Pool row of list entry `pos` of sequence `seq`, or -1 (nothing listed, or a
 // position or page outside its range, which sets `bad`).
@@ -249,54 +265,72 @@ __device__ __forceinline__ int slot_of(const AttendParams& p, const int32_t* tab
 }
 
 // Query rows to shared memory as the MMA reads them (see the file's comment),
-// row by row over `n_warps` warps.
+// row by row over n_warps warps, the loads of two rows in flight.
 template <int NH>
 __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
                                               int warp, int n_warps, int lane) {
   using L = AttSmem<NH>;
   constexpr int kChunks = kKvQ / 8;  // 16-byte chunks of a row: 64 latent, 8 rotary
-  for (int r = warp; r < NH; r += n_warps) {
-    const bool live = h0 + r < p.H;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (t * p.H + h0 + r) * kKvQ);
-    uint4 v[3];
+  for (int r0 = warp; r0 < NH; r0 += 2 * n_warps) {
+    uint4 v[2][3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      v[i] = live && lane + 32 * i < kChunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-    uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
+    for (int w = 0; w < 2; ++w) {
+      const int r = r0 + w * n_warps;
+      const bool live = r < NH && h0 + r < p.H;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (t * p.H + h0 + r) * kKvQ);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      m = __vmaxu2(m, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-      m = __vmaxu2(m, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+      for (int i = 0; i < 3; ++i)
+        v[w][i] = live && lane + 32 * i < kChunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     }
-    m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
-    const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    if (lane == 0) s_c[r] = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int c = lane + 32 * i;
-      if (c < kChunks) {
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[4];
+    for (int w = 0; w < 2; ++w) {
+      const int r = r0 + w * n_warps;
+      if (r >= NH) break;
+      uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
-          if (c < kKvLat / 8) {
-            const __half2 h = __floats2half2_rn(a, b);
-            o[k] = *reinterpret_cast<const uint32_t*>(&h);
-          } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 3; ++i) {
+        m = __vmaxu2(m, __vmaxu2(v[w][i].x & 0x7FFF7FFFu, v[w][i].y & 0x7FFF7FFFu));
+        m = __vmaxu2(m, __vmaxu2(v[w][i].z & 0x7FFF7FFFu, v[w][i].w & 0x7FFF7FFFu));
+      }
+      m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
+      const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      if (lane == 0) s_c[r] = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int c = lane + 32 * i;
+        if (c < kChunks) {
+          const uint32_t u[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
+            if (c < kKvLat / 8) {
+              const __half2 h = __floats2half2_rn(a, b);
+              o[k] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+              o[k] = *reinterpret_cast<const uint32_t*>(&h);
+            }
           }
+          // column block and 16-byte chunk of latent dimensions 8 c .. 8 c + 7 (the order of the decoded tiles)
+          const int blk = c < kKvLat / 8 ? 2 * part_dim((c >> 2) & 3) + (c >> 5) : 8;
+          const int at = c < kKvLat / 8 ? ((c >> 2) & 4) + (c & 3) : c & 7;
+          *reinterpret_cast<uint4*>(smem + blk * L::q_block + r * 128 + ((at ^ (r & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
-        // column block and 16-byte chunk of latent dimensions 8 c .. 8 c + 7 (the order of the decoded tiles)
-        const int blk = c < kKvLat / 8 ? ((c >> 1) & 6) + (c >> 5) : 8;
-        const int at = c < kKvLat / 8 ? ((c >> 2) & 4) + (c & 3) : c & 7;
-        *reinterpret_cast<uint4*>(smem + blk * L::q_block + r * 128 + ((at ^ (r & 7)) << 4)) =
-            make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
+}
+
+// Float4 of a partial output block: 16 rows (dimensions) x NH columns (heads)
+// of part s, warp quarter p and half, column group j of 8 heads: a lane's
+// float4 holds rows lane / 4 and lane / 4 + 8 at heads 8 j + 2 (lane % 4) and
+// the next.
+template <int NH>
+__device__ __forceinline__ int64_t part_index(int64_t item, int s, int p, int half, int j, int lane) {
+  return ((((item * kParts + s) * 4 + p) * 2 + half) * (NH / 8) + j) * 32 + lane;
 }
 
 template <int NH>
@@ -342,7 +376,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 
   if (tid == 0) {
     for (int i = 0; i < 2 * kParts; ++i) {
-      mbar_init(bars + 8 * i, kLoadWarps);
+      mbar_init(bars + 8 * i, kLoadWarps / 2);
       mbar_init(bars + 8 * (2 * kParts + i), 1);
     }
     mbar_init(bar_s(0), 1);
@@ -363,77 +397,143 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   }
   __syncthreads();
 
-  const int lw = warp - kSoftWarps, key = lw * 8 + (lane & 7), part = lane >> 3;
-  if (warp < kMmaWarp) {
-    stage_queries<NH>(p, t, h0, smem, s_c, warp, kMmaWarp, lane);
-    fence_proxy_async_smem();
+  if (warp <= kMmaWarp) {
+    if (warp < kMmaWarp) {
+      stage_queries<NH>(p, t, h0, smem, s_c, warp, kMmaWarp, lane);
+      fence_proxy_async_smem();
+    }
     tc_fence_before();
-    named_bar_sync(2, (kMmaWarp + 1) * 32);
+    named_bar_sync(2, kWorkThreads + 32);
     tc_fence_after();
   }
-  if (warp == kListWarp) {
-    // --------------------------------------------------------------- list
-    // Packs the pool rows of the entries that name a key into tiles, ahead of
-    // the gathering warps; a tile of 0 keys ends the list.
-    const int32_t* table = p.block_table + static_cast<int64_t>(seq) * p.max_blocks;
-    int total = 0;  // keys packed; total / kKt tiles are published
-    bool ok = true, bad = false;
-    auto open_tile = [&](int tile) {  // before the first write to a ring tile
-      return __all_sync(~0u, mbar_wait(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
-    };
-    auto publish = [&](int tile, int count) {
-      if (lane == 0) s_ring_n[tile % kRing] = count;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
-    };
-    int pos[4];
-    auto fetch = [&](int j0) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
-    };
-    fetch(j_lo);
-    for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
-      int slot[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) slot[k] = slot_of(p, table, pos[k], bad);
-      fetch(j0 + 128);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
-        const int cnt = __popc(m), at = total + __popc(m & lanemask_lt()), end = total + cnt;
-        if (cnt == 0) continue;
-        // a tile is opened by the batch that writes its first key
-        const int first = (total + kKt - 1) / kKt, last = (end - 1) / kKt;
-        if (last >= first && !(ok = open_tile(last))) break;
-        if (slot[k] >= 0) s_ring[at % (kRing * kKt)] = slot[k];
+  // each warpgroup's share of the registers, set on its own path (behind a join
+  // of the paths the compiler would hold all of them to the smallest)
+  if (warp >= kMmaWarp) {
+    regs_dec<kIssueRegs>();
+    if (warp == kListWarp) {
+      // --------------------------------------------------------------- list
+      // Packs the pool rows of the entries that name a key into tiles, ahead of
+      // the gathering warps; a tile of 0 keys ends the list.
+      const int32_t* table = p.block_table + static_cast<int64_t>(seq) * p.max_blocks;
+      int total = 0;  // keys packed; total / kKt tiles are published
+      bool ok = true, bad = false;
+      auto open_tile = [&](int tile) {  // before the first write to a ring tile
+        return __all_sync(~0u, mbar_wait(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
+      };
+      auto publish = [&](int tile, int count) {
+        if (lane == 0) s_ring_n[tile % kRing] = count;
         __syncwarp();
-        if (end / kKt > total / kKt) publish(total / kKt, kKt);
-        total = end;
+        if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
+      };
+      int pos[4];
+      auto fetch = [&](int j0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
+      };
+      fetch(j_lo);
+      for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
+        int slot[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) slot[k] = slot_of(p, table, pos[k], bad);
+        fetch(j0 + 128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
+          const int cnt = __popc(m), at = total + __popc(m & lanemask_lt()), end = total + cnt;
+          if (cnt == 0) continue;
+          // a tile is opened by the batch that writes its first key
+          const int first = (total + kKt - 1) / kKt, last = (end - 1) / kKt;
+          if (last >= first && !(ok = open_tile(last))) break;
+          if (slot[k] >= 0) s_ring[at % (kRing * kKt)] = slot[k];
+          __syncwarp();
+          if (end / kKt > total / kKt) publish(total / kKt, kKt);
+          total = end;
+        }
       }
+      if (ok && total % kKt) {
+        publish(total / kKt, total % kKt);
+        total += kKt - total % kKt;
+      }
+      if (ok && open_tile(total / kKt)) publish(total / kKt, 0);
+      if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- MMA
+      const uint32_t tmem = *s_tmem;
+      if (elect_one()) {
+        constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0), kIdR = idesc_att(64, NH, 1, 0), kIdO = idesc_att(128, NH, 0, 1);
+        // descriptors advance by their 16-byte address field
+        const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ), dV = desc_mn_sw128(sK, kBlockBytes),
+                       dP = desc_mn_sw128(sP, kBlockBytes);
+        bool ok = true;
+        auto output = [&](int i) {  // O^T += V^T P^T of tile i
+          const int b = i & 1;
+          if (!mbar_wait(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
+          tc_fence_after();
+#pragma unroll 1  // 4 x 4 MMAs: unrolled, their descriptors spill
+          for (int s = 0; s < kParts; ++s) {
+            const uint64_t v = dV + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4);
+#pragma unroll
+            for (int k = 0; k < kKt / 16; ++k)
+              mma_bf16(tmem + kTmemO + s * NH, v + (k * 2048 >> 4), dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
+            mma_commit(bar_empty(b, s));
+          }
+          mma_commit(bar_o);
+          return true;
+        };
+        int i = 0;
+        for (; ok; ++i) {
+          const int b = i & 1;
+          const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
+          if (!(ok = mbar_wait(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
+#pragma unroll 1
+          for (int s = 0; s < kParts; ++s) {
+            if (s > 0 && !(ok = mbar_wait(bar_full(b, s), ph, s_abort, g.err))) break;
+            tc_fence_after();
+            const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16(d, k0 + (((k >> 2) * kBlockBytes + 32 * (k & 3)) >> 4),
+                       q0 + (((k >> 2) * L::q_block + 32 * (k & 3)) >> 4), kIdS, s > 0 || k > 0);
+            if (s == 1) {  // each group brings half of the rotary block with its first part
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_bf16(d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4), dQ + ((8 * L::q_block + 32 * k) >> 4),
+                         kIdR, 1);
+            }
+          }
+          if (!ok) break;
+          mma_commit(bar_s(b));
+          if (i > 0) ok = output(i - 1);
+        }
+        if (ok && i > 0) output(i - 1);
+        // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+        mma_commit(bar_drain);
+        int unused = 0;
+        mbar_wait(bar_drain, 0, &unused, g.err);
+      }
+      __syncwarp();
     }
-    if (ok && total % kKt) {
-      publish(total / kKt, total % kKt);
-      total += kKt - total % kKt;
-    }
-    if (ok && open_tile(total / kKt)) publish(total / kKt, 0);
-    if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
-  } else if (warp >= kSoftWarps && warp < kMmaWarp) {
+  } else if (warp >= kSoftWarps) {
+    regs_dec<kLoadRegs>();
+    const uint32_t tmem = *s_tmem;
     // ------------------------------------------------------------- gather
+    const int lw = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3;
+    const int key = lw * 8 + (lane & 7), part = lane >> 3;
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
     RawKey raw;
     int n_keys = 0;
-    bool ok = true;
     auto take = [&](RawKey& r, int& count, int tile) {  // a tile's loads, once its slots are listed
       const int k = tile % kRing;
       if (!__all_sync(~0u, mbar_wait(bar_listed(k), static_cast<uint32_t>(tile / kRing) & 1u, s_abort, g.err))) return false;
       count = s_ring_n[k];
-      load_raw(r, p.kv, s_ring[k * kKt + key], key < count, part);
+      load_raw(r, p.kv, s_ring[k * kKt + key], key < count, part, group);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_taken(k));
       return true;
     };
-    ok = take(raw, n_keys, 0);
-    for (int i = 0; ok; ++i) {
+    bool ok = take(raw, n_keys, 0);
+    int i = 0;
+    for (; ok; ++i) {
       const int b = i & 1;
       const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
       RawKey next;
@@ -441,22 +541,21 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       if (n_keys > 0 && !(ok = take(next, n_next, i + 1))) break;
       const uint32_t tile = sK + b * kTileBytes + row;
 #pragma unroll
-      for (int s = 0; s < kParts; ++s) {
+      for (int u = 0; u < kParts / 2; ++u) {
+        const int s = 2 * u + group;
         if (!(ok = __all_sync(~0u, mbar_wait(bar_empty(b, s), ph, s_abort, g.err)))) break;
-        if (s == 0) {
-          if (lw == 0 && lane == 0) s_n[b] = n_keys;
-          const uint32_t dst = tile + 8 * kBlockBytes;
-          sts128(dst + (((2 * part) ^ sw) << 4), raw.rope[0], raw.rope[1], raw.rope[2], raw.rope[3]);
-          sts128(dst + (((2 * part + 1) ^ sw) << 4), raw.rope[4], raw.rope[5], raw.rope[6], raw.rope[7]);
+        if (u == 0) {
+          if (warp == kSoftWarps && lane == 0) s_n[b] = n_keys;
+          sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
         }
-        const uint32_t sw2 = (s < 2 ? raw.scale.x : raw.scale.y) >> (16 * (s & 1));
-        const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(sw2 & 0xFFFFu), __NV_E4M3));
+        const __half2 sc = __half2(
+            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((raw.scale >> (16 * u)) & 0xFFFFu), __NV_E4M3));
         const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
         const uint32_t dst = tile + (2 * s + (part >> 1)) * kBlockBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t o[4];
-          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
+          decode8(raw.code[4 * u + k], k < 2 ? lo : hi, o);
           sts128(dst + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
@@ -468,219 +567,226 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       raw = next;
       n_keys = n_next;
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- MMA
-    named_bar_sync(2, (kMmaWarp + 1) * 32);
+    // ------------------------------------------------------------- output
+    // Warpgroup s takes part s: O^T from TMEM as 8 x 8 fragments with heads as
+    // columns, stored transposed to the tile buffers (nothing reads those any
+    // more), then one 1 KB bulk copy per head.
+    named_bar_sync(3, kWorkThreads);
     tc_fence_after();
-    const uint32_t tmem = *s_tmem;
-    if (elect_one()) {
-      constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0), kIdR = idesc_att(64, NH, 1, 0), kIdO = idesc_att(128, NH, 0, 1);
-      // descriptors advance by their 16-byte address field
-      const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ), dV = desc_mn_sw128(sK, kBlockBytes),
-                     dP = desc_mn_sw128(sP, kBlockBytes);
-      bool ok = true;
-      auto output = [&](int i) {  // O^T += V^T P^T of tile i
-        const int b = i & 1;
-        if (!mbar_wait(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
-        tc_fence_after();
+    const int s = (warp - kSoftWarps) >> 2, pq = warp & 3;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      uint32_t o[NH / 2];
+      if (i > 0) {
+        tmem_ld_tile(tmem + kTmemO + s * NH + (static_cast<uint32_t>(pq * 32 + half * 16) << 16), o);
+        tmem_wait_ld();
+      } else {
 #pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-#pragma unroll
-          for (int k = 0; k < kKt / 16; ++k)
-            mma_bf16(tmem + kTmemO + s * NH, dV + ((b * kTileBytes + 2 * s * kBlockBytes + k * 2048) >> 4),
-                     dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
-          mma_commit(bar_empty(b, s));
-        }
-        mma_commit(bar_o);
-        return true;
-      };
-      int i = 0;
-      for (; ok; ++i) {
-        const int b = i & 1;
-        const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
-        if (!(ok = mbar_wait(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
-#pragma unroll
-        for (int s = 0; s < kParts; ++s) {
-          if (s > 0 && !(ok = mbar_wait(bar_full(b, s), ph, s_abort, g.err))) break;
-          tc_fence_after();
-          if (s == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_bf16(d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4), dQ + ((8 * L::q_block + 32 * k) >> 4),
-                       kIdR, k > 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int blk = 2 * s + (k >> 2);
-            mma_bf16(d, dK + ((b * kTileBytes + blk * kBlockBytes + 32 * (k & 3)) >> 4),
-                     dQ + ((blk * L::q_block + 32 * (k & 3)) >> 4), kIdS, 1);
-          }
-        }
-        if (!ok) break;
-        mma_commit(bar_s(b));
-        if (i > 0) ok = output(i - 1);
+        for (int k = 0; k < NH / 2; ++k) o[k] = 0u;
       }
-      if (ok && i > 0) output(i - 1);
-      // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
-      mma_commit(bar_drain);
-      int unused = 0;
-      mbar_wait(bar_drain, 0, &unused, g.err);
+      if (g.splits > 1) {
+#pragma unroll
+        for (int j = 0; j < NH / 8; ++j)
+          g.part_o[part_index<NH>(item, s, pq, half, j, lane)] =
+              make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                          __uint_as_float(o[4 * j + 3]));
+      } else {
+        const int dim = 128 * pq + 32 * part_dim(s) + 16 * half + (lane & 8);
+#pragma unroll
+        for (int j = 0; j < NH / 8; j += 2) {
+          uint32_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = *reinterpret_cast<const float2*>(s_f + 8 * (j + (k >> 1)) + 2 * (lane & 3));
+            const int x = 4 * j + 2 * k;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[x]) * f.x, __uint_as_float(o[x + 1]) * f.y);
+            v[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          stmatrix_t4(sK + (8 * (j + (lane >> 4)) + (lane & 7)) * kOutRow + 2 * dim, v);
+        }
+      }
     }
-    __syncwarp();
-  } else if (warp < kSoftWarps) {
+    tc_fence_before();
+    if (g.splits == 1) {
+      fence_proxy_async_smem();
+      named_bar_sync(4, kLoadWarps * 32);
+      const int h = tid - kSoftWarps * 32;
+      if (h < NH && h0 + h < p.H) {
+        bulk_store(p.out + (t * p.H + h0 + h) * kKvLat, sK + h * kOutRow, 2 * kKvLat);
+        bulk_store_wait();
+      }
+    }
+  } else {
+    regs_inc<kSoftRegs>();
+    const uint32_t tmem = *s_tmem;
     // ------------------------------------------------------------ softmax
-    constexpr int C = NH / 4;  // columns per thread
-    float c[C], m[C], l[C];
+    // Threads hold pairs of columns (heads): pair j is columns 8 j + 2 (lane %
+    // 4) and the next, at keys (rows) r0 and r0 + 8 of the warp's 16.
+    constexpr int C = NH / 8;
+    float2 c[C], m[C], l[C];  // factor to log2 units, negated reference, sum
 #pragma unroll
     for (int j = 0; j < C; ++j) {
-      c[j] = s_c[(j >> 1) * 8 + 2 * (lane & 3) + (j & 1)];
-      m[j] = -INFINITY;
-      l[j] = 0.f;
+      c[j] = *reinterpret_cast<const float2*>(s_c + 8 * j + 2 * (lane & 3));
+      m[j] = make_float2(INFINITY, INFINITY);
+      l[j] = make_float2(0.f, 0.f);
     }
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t r0 = lane >> 2;
+    const int r0 = lane >> 2;
     const uint32_t p0 = sP + (warp * 16 + r0) * 128 + (lane & 3) * 4;
-    const uint32_t tmem = *s_tmem;
+    float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH], while P is not in use
     bool ok = true;
     int nt = 0;  // tiles
     for (int i = 0;; nt = ++i) {
       const int b = i & 1;
       ok = __all_sync(~0u, mbar_wait(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const int n_keys = ok ? s_n[b] : 0;
-      const bool v0 = warp * 16 + static_cast<int>(r0) < n_keys, v1 = warp * 16 + 8 + static_cast<int>(r0) < n_keys;
       if (n_keys > 0)
         ok = __all_sync(~0u, mbar_wait(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const bool end = !ok || n_keys == 0;
-      tc_fence_after();
-      uint32_t x[NH / 2];
-      if (n_keys > 0) {
-        tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, x);
-        tmem_wait_ld();
-      }
       bool rise = end;
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const int k = 4 * (j >> 1) + (j & 1);
-        const float a = fmaf(__uint_as_float(x[k]), c[j], -m[j]), d = fmaf(__uint_as_float(x[k + 2]), c[j], -m[j]);
-        rise |= (v0 && a > kRise) || (v1 && d > kRise);
-      }
-      // the same decision in all four warps; the end of the list and a wait that gave up go this way too
-      if (soft_bar_or(rise)) {
-        if (i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
-        if (soft_bar_or(end || !ok)) break;
-        float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH]: P of the last tile is consumed
+      float x[NH / 2];
+      auto scores = [&] {  // x <- score - reference, -inf behind the last key; the largest
+        uint32_t u[NH / 2];
+        tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, u);
+        tmem_wait_ld();
+        float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          const int k = 4 * (j >> 1) + (j & 1);
-          float mx = fmaxf(v0 ? __uint_as_float(x[k]) * c[j] : -INFINITY, v1 ? __uint_as_float(x[k + 2]) * c[j] : -INFINITY);
+          const float2 a = __ffma2_rn(make_float2(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1])), c[j], m[j]);
+          const float2 d = __ffma2_rn(make_float2(__uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3])), c[j], m[j]);
+          x[4 * j] = a.x;
+          x[4 * j + 1] = a.y;
+          x[4 * j + 2] = d.x;
+          x[4 * j + 3] = d.y;
+        }
+        if (n_keys < kKt) {
+          const bool v0 = warp * 16 + r0 < n_keys, v1 = warp * 16 + 8 + r0 < n_keys;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-          if (lane < 4) exch[warp * NH + (j >> 1) * 8 + 2 * lane + (j & 1)] = mx;
+          for (int k = 0; k < NH / 2; ++k)
+            if (!(k & 2 ? v1 : v0)) x[k] = -INFINITY;
+        }
+#pragma unroll
+        for (int k = 0; k < NH / 2; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+        return mx;
+      };
+      if (!end) {
+        tc_fence_after();
+        rise = scores() > kRise;
+      }
+      // the same decision in all four warps; the end of the list and a wait that gave up go this way too
+      const bool moved = soft_bar_or(rise);
+      if (moved) {
+        if (i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+        if (soft_bar_or(end || !ok)) break;
+        tc_fence_after();
+        {
+          uint32_t u[NH / 2];
+          tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, u);
+          tmem_wait_ld();
+          const bool v0 = warp * 16 + r0 < n_keys, v1 = warp * 16 + 8 + r0 < n_keys;
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            float2 mx = make_float2(-INFINITY, -INFINITY);
+            if (v0) mx = make_float2(__uint_as_float(u[4 * j]) * c[j].x, __uint_as_float(u[4 * j + 1]) * c[j].y);
+            if (v1) {
+              mx.x = fmaxf(mx.x, __uint_as_float(u[4 * j + 2]) * c[j].x);
+              mx.y = fmaxf(mx.y, __uint_as_float(u[4 * j + 3]) * c[j].y);
+            }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              mx.x = fmaxf(mx.x, __shfl_xor_sync(~0u, mx.x, o));
+              mx.y = fmaxf(mx.y, __shfl_xor_sync(~0u, mx.y, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = mx;
+          }
         }
         named_bar_sync(1, kSoftThreads);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          const int col = (j >> 1) * 8 + 2 * (lane & 3) + (j & 1);
-          const float mn = fmaxf(fmaxf(fmaxf(exch[col], exch[NH + col]), fmaxf(exch[2 * NH + col], exch[3 * NH + col])), m[j]);
-          const float f = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
-          m[j] = mn;
-          l[j] *= f;
-          if (warp == 0 && lane < 4) s_f[col] = f;
+          const int col = 8 * j + 2 * (lane & 3);
+          float2 n = make_float2(-m[j].x, -m[j].y), f = make_float2(1.f, 1.f);
+#pragma unroll
+          for (int w = 0; w < kSoftWarps; ++w) {
+            const float2 e = *reinterpret_cast<const float2*>(exch + w * NH + col);
+            n.x = fmaxf(n.x, e.x);
+            n.y = fmaxf(n.y, e.y);
+          }
+          if (n.x != -INFINITY) f.x = ex2(-m[j].x - n.x);
+          if (n.y != -INFINITY) f.y = ex2(-m[j].y - n.y);
+          m[j] = make_float2(-n.x, -n.y);
+          l[j].x *= f.x;
+          l[j].y *= f.y;
+          if (warp == 0 && lane < 4) *reinterpret_cast<float2*>(s_f + col) = f;
         }
         named_bar_sync(1, kSoftThreads);
         if (i > 0) {
+#pragma unroll 1
           for (int q = 0; q < kParts * NH; q += 16) {
             uint32_t o[16];
             tmem_ld16(tmem + kTmemO + lane_base + q, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s_f[(q + k) % NH]);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s_f[q % NH + k]);
             tmem_st16(tmem + kTmemO + lane_base + q, o);
           }
           tmem_wait_st();
         }
-      } else if (i > 0) {
-        ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+        scores();
       }
+      uint32_t w[NH / 4];
 #pragma unroll
-      for (int j = 0; j < C; j += 2) {
-        const int k = 2 * j;
-        const float a0 = v0 ? ex2(fmaf(__uint_as_float(x[k]), c[j], -m[j])) : 0.f;
-        const float a1 = v0 ? ex2(fmaf(__uint_as_float(x[k + 1]), c[j + 1], -m[j + 1])) : 0.f;
-        const float d0 = v1 ? ex2(fmaf(__uint_as_float(x[k + 2]), c[j], -m[j])) : 0.f;
-        const float d1 = v1 ? ex2(fmaf(__uint_as_float(x[k + 3]), c[j + 1], -m[j + 1])) : 0.f;
-        l[j] += a0 + d0;
-        l[j + 1] += a1 + d1;
-        const __half2 ha = __floats2half2_rn(a0, a1), hd = __floats2half2_rn(d0, d1);
-        const uint32_t at = p0 + (((j >> 1) ^ r0) << 4);
-        sts32(at, *reinterpret_cast<const uint32_t*>(&ha));
-        sts32(at + 8 * 128, *reinterpret_cast<const uint32_t*>(&hd));
+      for (int j = 0; j < C; ++j) {
+        const float2 a = make_float2(ex2(x[4 * j]), ex2(x[4 * j + 1])), d = make_float2(ex2(x[4 * j + 2]), ex2(x[4 * j + 3]));
+        l[j] = __fadd2_rn(l[j], __fadd2_rn(a, d));
+        const __half2 ha = __floats2half2_rn(a.x, a.y), hd = __floats2half2_rn(d.x, d.y);
+        w[2 * j] = *reinterpret_cast<const uint32_t*>(&ha);
+        w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hd);
+      }
+      // P of the last tile is consumed (checked above when the reference moved)
+      if (!moved && i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        sts32(p0 + ((j ^ r0) << 4), w[2 * j]);
+        sts32(p0 + ((j ^ r0) << 4) + 8 * 128, w[2 * j + 1]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_p);
     }
-    // ------------------------------------------------------------- output
-    if (nt > 0) mbar_wait(bar_o, static_cast<uint32_t>(nt - 1) & 1u, s_abort, g.err);
-    __syncwarp();
-    tc_fence_after();
-    float* exch = reinterpret_cast<float*>(smem + L::off_p);
+    // --------------------------------------------------------- statistics
+    // (the loop ended behind the last product: P is not in use)
     named_bar_sync(1, kSoftThreads);
 #pragma unroll
     for (int j = 0; j < C; ++j) {
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(~0u, l[j], o);
-      if (lane < 4) exch[warp * NH + (j >> 1) * 8 + 2 * lane + (j & 1)] = l[j];
+      for (int o = 4; o < 32; o <<= 1) {
+        l[j].x += __shfl_xor_sync(~0u, l[j].x, o);
+        l[j].y += __shfl_xor_sync(~0u, l[j].y, o);
+      }
+      if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = l[j];
     }
     named_bar_sync(1, kSoftThreads);
     if (warp == 0 && lane < 4) {
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        const int col = (j >> 1) * 8 + 2 * lane + (j & 1);
-        const float sum = (exch[col] + exch[NH + col]) + (exch[2 * NH + col] + exch[3 * NH + col]);
-        if (g.splits > 1) {
-          g.part_ml[item * NH + col] = make_float2(m[j], sum);
-          s_f[col] = 1.f;
-        } else {
-          s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
-          if (p.lse && h0 + col < p.H)
-            p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (m[j] + log2f(sum)) * 0.69314718055994531f;
-        }
-      }
-    }
-    named_bar_sync(1, kSoftThreads);
-    for (int s = 0; s < kParts; ++s) {
-      const int dim = warp * 128 + s * 32 + lane;
-      for (int q = 0; q < NH; q += 16) {
-        if (h0 + q >= p.H) break;
-        uint32_t o[16];
-        if (nt > 0) {
-          tmem_ld16(tmem + kTmemO + s * NH + lane_base + q, o);
-          tmem_wait_ld();
-        } else {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = 0u;
-        }
-        if (g.splits > 1) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (h0 + q + k < p.H) g.part_o[(item * NH + q + k) * kKvLat + dim] = __uint_as_float(o[k]);
-        } else {
-          // lanes pair up: the even one stores two dimensions of head q + k, the odd one of q + k + 1
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            const float a = __uint_as_float(o[k]) * s_f[q + k], b = __uint_as_float(o[k + 1]) * s_f[q + k + 1];
-            const float other = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
-            const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, b) : __floats2bfloat162_rn(a, other);
-            const int h = h0 + q + k + (lane & 1);
-            if (h < p.H)
-              *reinterpret_cast<__nv_bfloat162*>(p.out + (t * p.H + h) * kKvLat + (dim & ~1)) = v;
+        for (int k = 0; k < 2; ++k) {
+          const int col = 8 * j + 2 * lane + k;
+          const float ref = k ? -m[j].y : -m[j].x;
+          const float sum = (exch[col] + exch[NH + col]) + (exch[2 * NH + col] + exch[3 * NH + col]);
+          if (g.splits > 1) {
+            g.part_ml[item * NH + col] = make_float2(ref, sum);
+          } else {
+            s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
+            if (p.lse && h0 + col < p.H)
+              p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
           }
         }
       }
     }
     tc_fence_before();
+    named_bar_sync(3, kWorkThreads);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -689,37 +795,62 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   }
 }
 
-// Joins the splits of one (row, head): out = sum_s 2^(m_s - m) O_s / sum_s
-// 2^(m_s - m) l_s.
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p, const AttGrid g, int NH) {
-  const int64_t t = blockIdx.x / p.H;
-  const int h = static_cast<int>(blockIdx.x % p.H);
+// Joins the splits of eight heads of a row and one part of their dimensions:
+// out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s.
+template <int NH>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, const AttGrid g) {
+  __shared__ __align__(16) uint16_t s_o[8][128 + 8];
+  const int s = blockIdx.x % kParts, j = blockIdx.x / kParts % (NH / 8);
+  const int64_t row = blockIdx.x / (kParts * (NH / 8));
+  const int hb = static_cast<int>(row % g.head_blocks);
+  const int64_t t = row / g.head_blocks;
   const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
-  if (seq < 0 || seq >= p.B) return;
-  const int64_t item0 = (t * g.head_blocks + h / NH) * g.splits;
-  const int col = h % NH;
-  float m = -INFINITY;
-  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.part_ml[(item0 + s) * NH + col].x);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < g.splits; ++s) {
-    const float2 ml = g.part_ml[(item0 + s) * NH + col];
-    const float w = ex2(ml.x - ref);
-    const float4 o = reinterpret_cast<const float4*>(g.part_o + ((item0 + s) * NH + col) * kKvLat)[threadIdx.x];
-    sum = fmaf(w, ml.y, sum);
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
+  const int h0 = hb * NH + 8 * j;
+  if (seq < 0 || seq >= p.B || h0 >= p.H) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pq = warp & 3, half = warp >> 2;
+  const int64_t item0 = row * g.splits;
+  const float4* ml = reinterpret_cast<const float4*>(g.part_ml + item0 * NH + 8 * j + 2 * (lane & 3));  // two heads
+  constexpr int kMl = NH / 2;                                 // float4 between splits
+  constexpr int64_t kO = int64_t(NH) * kKvLat / 4;
+  const float4* po = g.part_o + part_index<NH>(item0, s, pq, half, j, lane);
+  float2 ref = make_float2(-INFINITY, -INFINITY);
+  for (int k = 0; k < g.splits; ++k) {
+    const float4 v = ml[static_cast<int64_t>(k) * kMl];
+    ref.x = fmaxf(ref.x, v.x);
+    ref.y = fmaxf(ref.y, v.z);
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kKvLat)[threadIdx.x] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (p.lse && threadIdx.x == 0)
-    p.lse[t * p.H + h] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+  const float2 base = make_float2(ref.x == -INFINITY ? 0.f : ref.x, ref.y == -INFINITY ? 0.f : ref.y);
+  float2 sum = make_float2(0.f, 0.f);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < g.splits; ++k) {
+    const float4 v = ml[static_cast<int64_t>(k) * kMl], o = po[k * kO];
+    const float a = ex2(v.x - base.x), b = ex2(v.z - base.y);
+    sum.x = fmaf(a, v.y, sum.x);
+    sum.y = fmaf(b, v.w, sum.y);
+    acc.x = fmaf(a, o.x, acc.x);
+    acc.y = fmaf(b, o.y, acc.y);
+    acc.z = fmaf(a, o.z, acc.z);
+    acc.w = fmaf(b, o.w, acc.w);
+  }
+  const float fa = sum.x == 0.f ? 0.f : 1.f / sum.x, fb = sum.y == 0.f ? 0.f : 1.f / sum.y;
+  const int r = 32 * pq + 16 * half + (lane >> 2), col = 2 * (lane & 3);
+  s_o[col][r] = __bfloat16_as_ushort(__float2bfloat16_rn(acc.x * fa));
+  s_o[col + 1][r] = __bfloat16_as_ushort(__float2bfloat16_rn(acc.y * fb));
+  s_o[col][r + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(acc.z * fa));
+  s_o[col + 1][r + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(acc.w * fb));
+  if (p.lse && s == 0 && warp == 0 && lane < 4) {
+    if (h0 + col < p.H)
+      p.lse[t * p.H + h0 + col] = sum.x == 0.f ? -INFINITY : (base.x + log2f(sum.x)) * 0.69314718055994531f;
+    if (h0 + col + 1 < p.H)
+      p.lse[t * p.H + h0 + col + 1] = sum.y == 0.f ? -INFINITY : (base.y + log2f(sum.y)) * 0.69314718055994531f;
+  }
+  __syncthreads();
+  if (threadIdx.x < 128 && h0 + (threadIdx.x >> 4) < p.H) {  // 16 bytes: 8 dimensions of a head
+    const int h = threadIdx.x >> 4, c = threadIdx.x & 15;
+    *reinterpret_cast<uint4*>(p.out + (t * p.H + h0 + h) * kKvLat + 128 * (c >> 2) + 32 * part_dim(s) + 8 * (c & 3)) =
+        *reinterpret_cast<const uint4*>(&s_o[h][8 * c]);
+  }
 }
 
 struct AttPlan {
@@ -752,6 +883,9 @@ cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   const int64_t grid = p.T * g.head_blocks * g.splits;
   attend_kv4_kernel<NH><<<static_cast<unsigned>(grid), kAttThreads, bytes, st>>>(p, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || g.splits == 1) return e;
+  attend_join_kernel<NH><<<static_cast<unsigned>(p.T * g.head_blocks * kParts * (NH / 8)), 256, 0, st>>>(p, g);
   return cudaGetLastError();
 }
 
@@ -762,12 +896,9 @@ size_t attend_workspace_bytes(int64_t T, int H, int n, int sms) { return plan_at
 cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st) {
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float*>(ws + P.off_o),
+  AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float4*>(ws + P.off_o),
             reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
-  cudaError_t e = P.NH == 16 ? launch_nh<16>(p, g, st) : P.NH == 32 ? launch_nh<32>(p, g, st) : launch_nh<64>(p, g, st);
-  if (e != cudaSuccess || P.splits == 1) return e;
-  attend_join_kernel<<<static_cast<unsigned>(p.T * p.H), 128, 0, st>>>(p, g, P.NH);
-  return cudaGetLastError();
+  return P.NH == 16 ? launch_nh<16>(p, g, st) : P.NH == 32 ? launch_nh<32>(p, g, st) : launch_nh<64>(p, g, st);
 }
 
 }  // namespace dsa
