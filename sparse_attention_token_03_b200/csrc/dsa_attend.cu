@@ -47,14 +47,9 @@
 //
 // Few rows: the list is split over blocks, each writes its fp32 O and (m, l),
 // and a second kernel joins them.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
-#include "dsa_ptx.cuh"
-#include "dsa_serve.cuh"
+#include "dsa_attend.cuh"
 
 namespace dsa {
 
@@ -74,9 +69,7 @@ constexpr uint32_t kSoftRegs = 136, kLoadRegs = 72, kIssueRegs = 56;
 static_assert(kSoftRegs * 128 + kLoadRegs * 512 + kIssueRegs * 128 <= 80 * kAttThreads, "register pool");
 constexpr int kRing = 4;                         // tiles of slots that the list warp may be ahead
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr float kRise = 8.f;                     // log2 of the largest P before the reference moves
 constexpr uint32_t kOutRow = 2 * kKvLat + 16;     // staged output row, padded against bank conflicts
-constexpr float kLog2e = 1.4426950408889634f;
 
 template <int NH>
 struct AttSmem {
@@ -106,31 +99,6 @@ struct AttGrid {
   uint32_t* err;
 };
 
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
-  // M- or N-major operand: rows of 64 consecutive M (N) elements, 8 K rows per
-  // 1024-byte atom; mn_stride between 64-element groups, 1024 between K groups
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
-// Instruction descriptors (kind::f16, fp32 accumulation): operand format 0 =
-// fp16, 1 = bf16; bits 15 and 16 mark M- and N-major operands.
-constexpr uint32_t idesc_att(int M, int N, uint32_t fmt, uint32_t mn_major) {
-  return (1u << 4) | (fmt << 7) | (fmt << 10) | (mn_major << 15) | (mn_major << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 16 lanes x NH columns of fp32: thread i holds rows i / 4 (values 4j, 4j + 1)
 // and i / 4 + 8 (4j + 2, 4j + 3) at columns 8j + 2 (i % 4) and the next.
 __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&r)[32]) {
@@ -157,16 +125,6 @@ __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // Barrier over the softmax warps that also combines a predicate.
 __device__ __forceinline__ bool soft_bar_or(bool v) {
   uint32_t r;
@@ -179,9 +137,6 @@ __device__ __forceinline__ bool soft_bar_or(bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 // Four 8 x 8 matrices of 16-bit fragments, transposed: lane 8 i + r gives the
 // address of column r of matrix i.
 __device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&v)[4]) {
@@ -196,28 +151,6 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
 __device__ __forceinline__ void bulk_store_wait() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
-}
-
-// Eight E2M1 codes of a word to four fp16 pairs, times the block's scale pair.
-__device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
-  uint32_t v[4];
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-      : "r"(w));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&v[i]), s);
-    o[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
 // A key's raw bytes as one of its eight lanes (two groups of four) holds them:
 // 64 codes, their four scales and 8 rotary values.
 struct RawKey {
@@ -225,12 +158,6 @@ struct RawKey {
   uint32_t scale;
   uint4 rope;
 };
-
-__device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
-  asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "l"(p));
-}
 
 __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot, bool live, int part, int group) {
   if (live) {
@@ -251,75 +178,25 @@ __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot,
 // + r holds dimension 128 p + 32 part_dim(s) + r (the map is its own inverse).
 __device__ __forceinline__ constexpr int part_dim(int s) { return 2 * (s & 1) + (s >> 1); }
 
-// Pool row of list entry `pos` of sequence `seq`, or -1 (nothing listed, or a
-// position or page outside its range, which sets `bad`).
-__device__ __forceinline__ int slot_of(const AttendParams& p, const int32_t* table, int pos, bool& bad) {
-  if (pos < 0) return -1;
-  const int blk = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
-  if (blk < p.max_blocks) {
-    const int page = __ldg(table + blk);
-    if (page >= 0 && page < p.n_pages) return page * p.page_size + (pos - blk * p.page_size);
-  }
-  bad = true;
-  return -1;
-}
-
 // Query rows to shared memory as the MMA reads them (see the file's comment),
 // row by row over n_warps warps, the loads of two rows in flight.
 template <int NH>
 __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
                                               int warp, int n_warps, int lane) {
   using L = AttSmem<NH>;
-  constexpr int kChunks = kKvQ / 8;  // 16-byte chunks of a row: 64 latent, 8 rotary
   for (int r0 = warp; r0 < NH; r0 += 2 * n_warps) {
     uint4 v[2][3];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int r = r0 + w * n_warps;
       const bool live = r < NH && h0 + r < p.H;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (t * p.H + h0 + r) * kKvQ);
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        v[w][i] = live && lane + 32 * i < kChunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+      load_query_row(v[w], p, t, h0 + r, live, lane);
     }
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int r = r0 + w * n_warps;
       if (r >= NH) break;
-      uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        m = __vmaxu2(m, __vmaxu2(v[w][i].x & 0x7FFF7FFFu, v[w][i].y & 0x7FFF7FFFu));
-        m = __vmaxu2(m, __vmaxu2(v[w][i].z & 0x7FFF7FFFu, v[w][i].w & 0x7FFF7FFFu));
-      }
-      m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
-      const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-      if (lane == 0) s_c[r] = p.scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int c = lane + 32 * i;
-        if (c < kChunks) {
-          const uint32_t u[4] = {v[w][i].x, v[w][i].y, v[w][i].z, v[w][i].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
-            if (c < kKvLat / 8) {
-              const __half2 h = __floats2half2_rn(a, b);
-              o[k] = *reinterpret_cast<const uint32_t*>(&h);
-            } else {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-              o[k] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-          }
-          // column block and 16-byte chunk of latent dimensions 8 c .. 8 c + 7 (the order of the decoded tiles)
-          const int blk = c < kKvLat / 8 ? 2 * part_dim((c >> 2) & 3) + (c >> 5) : 8;
-          const int at = c < kKvLat / 8 ? ((c >> 2) & 4) + (c & 3) : c & 7;
-          *reinterpret_cast<uint4*>(smem + blk * L::q_block + r * 128 + ((at ^ (r & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
+      store_query_row(v[w], p.scale, smem, L::q_block, r, s_c, lane, part_dim);
     }
   }
 }
@@ -433,8 +310,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       fetch(j_lo);
       for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
         int slot[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) slot[k] = slot_of(p, table, pos[k], bad);
+          slots_of(p, table, pos, slot, bad);
         fetch(j0 + 128);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -460,7 +336,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       // ---------------------------------------------------------------- MMA
       const uint32_t tmem = *s_tmem;
       if (elect_one()) {
-        constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0), kIdR = idesc_att(64, NH, 1, 0), kIdO = idesc_att(128, NH, 0, 1);
+        constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0, 0), kIdR = idesc_att(64, NH, 1, 0, 0), kIdO = idesc_att(128, NH, 0, 1, 1);
         // descriptors advance by their 16-byte address field
         const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ), dV = desc_mn_sw128(sK, kBlockBytes),
                        dP = desc_mn_sw128(sP, kBlockBytes);
@@ -780,7 +656,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           } else {
             s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
             if (p.lse && h0 + col < p.H)
-              p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+              p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
           }
         }
       }
@@ -841,9 +717,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
   s_o[col + 1][r + 8] = __bfloat16_as_ushort(__float2bfloat16_rn(acc.w * fb));
   if (p.lse && s == 0 && warp == 0 && lane < 4) {
     if (h0 + col < p.H)
-      p.lse[t * p.H + h0 + col] = sum.x == 0.f ? -INFINITY : (base.x + log2f(sum.x)) * 0.69314718055994531f;
+      p.lse[t * p.H + h0 + col] = sum.x == 0.f ? -INFINITY : (base.x + log2f(sum.x)) * kLn2;
     if (h0 + col + 1 < p.H)
-      p.lse[t * p.H + h0 + col + 1] = sum.y == 0.f ? -INFINITY : (base.y + log2f(sum.y)) * 0.69314718055994531f;
+      p.lse[t * p.H + h0 + col + 1] = sum.y == 0.f ? -INFINITY : (base.y + log2f(sum.y)) * kLn2;
   }
   __syncthreads();
   if (threadIdx.x < 128 && h0 + (threadIdx.x >> 4) < p.H) {  // 16 bytes: 8 dimensions of a head
@@ -891,9 +767,12 @@ cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, cudaStream_t st) 
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t T, int H, int n, int sms) { return plan_attend(T, H, n, sms).bytes; }
+size_t attend_workspace_bytes(int64_t T, int H, int n, int sms) {
+  return H > 64 ? attend_pair_workspace_bytes(T, H, n, sms) : plan_attend(T, H, n, sms).bytes;
+}
 
 cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st) {
+  if (p.H > 64) return launch_attend_kv4_pair(p, workspace, sms, st);
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float4*>(ws + P.off_o),

@@ -1,0 +1,155 @@
+// Device parts shared by the attention kernels over the 4-bit latent cache
+// (dsa_attend.cu, dsa_attend_pair.cu): operand descriptors, decoding, query
+// staging and the list walk.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "dsa_ptx.cuh"
+#include "dsa_serve.cuh"
+
+namespace dsa {
+
+constexpr float kRise = 8.f;  // log2 of the largest P before the reference moves
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
+  // M- or N-major operand: rows of 64 consecutive M (N) elements, 8 K rows per
+  // 1024-byte atom; mn_stride between 64-element groups, 1024 between K groups
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((mn_stride >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptors (kind::f16, fp32 accumulation): operand format 0 =
+// fp16, 1 = bf16; bits 15 and 16 mark M- and N-major operands.
+constexpr uint32_t idesc_att(int M, int N, uint32_t fmt, uint32_t m_major, uint32_t n_major) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | (m_major << 15) | (n_major << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
+}
+
+// Eight E2M1 codes of a word to four fp16 pairs, times the block's scale pair.
+__device__ __forceinline__ void decode8(uint32_t w, __half2 s, uint32_t (&o)[4]) {
+  uint32_t v[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&v[i]), s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+__device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "l"(p));
+}
+
+// Pool rows of four list entries of a sequence (its block table `table`), or -1
+// where nothing is listed or the position or page is outside its range, which
+// sets `bad`.  The four table loads are in flight together.
+__device__ __forceinline__ void slots_of(const AttendParams& p, const int32_t* table, const int (&pos)[4], int (&slot)[4],
+                                         bool& bad) {
+  int blk[4], page[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    blk[k] = static_cast<int>(static_cast<uint32_t>(max(pos[k], 0)) / static_cast<uint32_t>(p.page_size));
+    page[k] = __ldg(table + min(blk[k], p.max_blocks - 1));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool in = blk[k] < p.max_blocks && page[k] >= 0 && page[k] < p.n_pages;
+    bad |= pos[k] >= 0 && !in;
+    slot[k] = pos[k] >= 0 && in ? page[k] * p.page_size + (pos[k] - blk[k] * p.page_size) : -1;
+  }
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A query row as its warp's lanes hold it: 72 16-byte chunks, 64 latent and 8
+// rotary; zeros for a head past the last.
+constexpr int kQChunks = kKvQ / 8;
+__device__ __forceinline__ void load_query_row(uint4 (&v)[3], const AttendParams& p, int64_t t, int h, bool live, int lane) {
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + (t * p.H + h) * kKvQ);
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    v[i] = live && lane + 32 * i < kQChunks ? __ldg(src + lane + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Row r of the staged queries: latent parts to fp16 and rotary parts to bf16,
+// both times the power of two that puts the row's largest magnitude in [2^14,
+// 2^15); s_c[r] takes the factor of its scores in log2 units.  Column block 2
+// order(s) + p / 2 (of q_block bytes) holds latent dimensions 128 p + 32 s ..
+// + 31 in its half p % 2; block 8 the rotary ones.
+template <typename Order>
+__device__ __forceinline__ void store_query_row(const uint4 (&v)[3], float scale, uint8_t* smem, uint32_t q_block, int r,
+                                                float* s_c, int lane, Order order) {
+  uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    m = __vmaxu2(m, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
+    m = __vmaxu2(m, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+  }
+  m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
+  const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  if (lane == 0) s_c[r] = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int c = lane + 32 * i;
+    if (c >= kQChunks) continue;
+    const bool rotary = c >= kKvLat / 8;
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
+      if (!rotary) {
+        const __half2 h = __floats2half2_rn(a, b);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        o[k] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    const int blk = rotary ? 8 : 2 * order((c >> 2) & 3) + (c >> 5);
+    const int at = rotary ? c & 7 : ((c >> 2) & 4) + (c & 3);
+    *reinterpret_cast<uint4*>(smem + blk * q_block + r * 128 + ((at ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+}  // namespace dsa

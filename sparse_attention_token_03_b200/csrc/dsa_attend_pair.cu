@@ -1,0 +1,744 @@
+// Attention over the selected keys of a 4-bit latent cache for more than 64
+// heads (dsa_attend.cu has the formulas and the kernel for up to 64): clusters
+// of two blocks work on one row, 128 of its heads and a range of its list, in
+// tiles of 128 keys, with MMAs over both blocks (cta_group::2),
+//
+//   S [128 heads x 128 keys]  = Q [128 x 576] K^T     (M = 128, N = 128, 36 K steps)
+//   O [128 heads x 512]      += P [128 x 128] V       (M = 128, N = 256, 2 x 8 K steps)
+//
+// Block c holds the queries of heads 64 c .. 64 c + 63, K of the tile's keys
+// 64 c .. 64 c + 63 (all dimensions) and V of all 128 keys (latent dimensions
+// 256 c .. 256 c + 255), and gets the scores and outputs of its heads: TMEM
+// lanes 0-63 the first half of a product's columns, lanes 64-127 the second.
+//
+// What bounds it is shared memory: with 64 heads per block on their own, a
+// 64-key tile moves 2560 wavefronts of 128 bytes (operands 1920, decoding
+// 640) against 1972 cycles of MMAs; here a 128-key tile of 128 heads moves
+// 3136 per block (operands 1920, decoding 1088, P 128) against 36 x 53 + 16 x
+// 65 = 2940 cycles, for twice the products.
+//
+//   warps 0-3    softmax and output; a thread has one head and half of the keys
+//                (output dimensions), so maxima and sums need no shuffles
+//   warps 4-11   decode K, eight keys a warp, handed over in four parts of 128
+//                dimensions; warps 12-19 decode V, 16 keys a warp, handed over
+//                in four parts of 32 keys
+//   warps 20-23  stage the queries of the next row
+//   warp 24      issues the MMAs (in the cluster's first block)
+//   warp 25      packs the pool rows of the list's entries into tiles
+//
+// K and V are single buffers that are never idle for long: the MMA order S(i
+// + 1), O(i) lets K be refilled during O and V during S.  The grid is
+// persistent: a cluster takes every n-th row, and the next row's queries,
+// keys and scores proceed while the last one's output is formed and stored.
+//
+// Numbers as in dsa_attend.cu: latents exact in fp16, queries fp16 after an
+// exact power of two, P fp16 relative to a reference at most 2^8 below the
+// running maximum, scores, sums and outputs fp32.
+#include <algorithm>
+
+#include "dsa_attend.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kTile = 128, kHalf = 64;            // keys of a tile; keys of K and heads of one block
+constexpr uint32_t kBlk = kHalf * 128;            // a 64-column block of K, Q or P
+constexpr uint32_t kVBlk = kTile * 128;           // a 64-column block of V
+constexpr int kNBlk = kKvQ / 64;
+constexpr int kK = 4, kV = 12, kQ = 20, kMma = 24, kList = 25;  // first warps of the roles, softmax from 0
+constexpr int kPairThreads = 28 * 32;
+constexpr int kPairRing = 4;                      // tiles that the list warp may be ahead
+// registers per thread: 72 at launch, then shared out by warpgroup
+constexpr uint32_t kSoftRegs = 96, kKRegs = 72, kVRegs = 64, kQRegs = 80, kIssueRegs = 56;
+static_assert(kSoftRegs * 128 + kKRegs * 256 + kVRegs * 256 + kQRegs * 128 + kIssueRegs * 128 <= 72 * kPairThreads,
+              "register pool");
+
+constexpr uint32_t kOffQ = 0, kOffK = kNBlk * kBlk, kOffV = 2 * kNBlk * kBlk, kOffP = kOffV + 4 * kVBlk;
+constexpr uint32_t kOffRing = kOffP + 2 * kBlk;                  // pool rows of the next tiles' keys
+constexpr uint32_t kOffMeta = kOffRing + kPairRing * kTile * 4;  // keys and flags of the next tiles
+constexpr uint32_t kOffC = kOffMeta + kPairRing * 4;             // per head: factor of a score in log2 units
+constexpr uint32_t kOffBars = kOffC + kHalf * 4;
+// barriers: K full, K empty, V full, V empty [4 parts each], listed, taken
+// [ring], scores [2], then P full, output done, Q full, Q empty, factors full,
+// factors empty, drain
+constexpr int kBarKF = 0, kBarKE = 4, kBarVF = 8, kBarVE = 12, kBarListed = 16, kBarTaken = kBarListed + kPairRing,
+              kBarS = kBarTaken + kPairRing, kBarP = kBarS + 2, kBarO = kBarP + 1, kBarQF = kBarO + 1, kBarQE = kBarQF + 1,
+              kBarCF = kBarQE + 1, kBarCE = kBarCF + 1, kBarDrain = kBarCE + 1, kBars = kBarDrain + 1;
+constexpr uint32_t kOffMisc = kOffBars + 8 * kBars;
+constexpr uint32_t kPairSmem = kOffMisc + 16;
+static_assert(kOffBars % 8 == 0 && kPairSmem <= 227u * 1024u, "shared memory layout");
+
+// Tile flags next to its number of keys.
+constexpr int kFirst = 1 << 16, kLast = 1 << 17, kStop = 1 << 18;
+
+struct PairGrid {
+  int head_blocks, splits, tiles;  // tiles: of a whole list
+  int64_t items;                   // T * head_blocks * splits
+  float* part_o;                   // [items][128][512]
+  float2* part_ml;                 // [items][128]
+  uint32_t* err;
+};
+
+// A cluster's next item with a row to work on: item k and what it stands for.
+struct PairItem {
+  int64_t k, t;
+  int hb, split, seq;
+};
+__device__ __forceinline__ bool next_item(PairItem& it, const AttendParams& p, const PairGrid& g, bool report) {
+  for (; it.k < g.items; it.k += gridDim.x >> 1) {
+    it.split = static_cast<int>(it.k % g.splits);
+    it.hb = static_cast<int>(it.k / g.splits % g.head_blocks);
+    it.t = it.k / g.splits / g.head_blocks;
+    it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
+    if (it.seq >= 0 && it.seq < p.B) return true;
+    if (it.seq >= p.B && report && p.status) atomicOr(p.status, kErrOverflow);  // else padding
+  }
+  return false;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The same barrier in the cluster's first block.
+__device__ __forceinline__ uint32_t in_first(uint32_t bar) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
+  return r;
+}
+// Block scope is enough here and at every wait: the blocks share no data but
+// what the MMAs read, which the writer's proxy fence orders before its arrival.
+// (Release and acquire of cluster scope cost a fence over the block's global
+// loads each, 7500 cycles a tile instead of 3700.)
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on this barrier of both blocks once the MMAs issued so far complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
+      : "memory");
+}
+// Barrier over the two softmax warps of the same heads, with a predicate.
+__device__ __forceinline__ bool heads_bar_or(int id, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+// 128 latent dimensions of a key: 64 bytes of codes and eight scales.
+struct RawLatent {
+  uint32_t code[16];
+  uint2 scale;
+};
+__device__ __forceinline__ void load_latent(RawLatent& r, const uint8_t* entry, int part) {
+  uint32_t a[8], b[8];
+  ldg256(a, entry + part * 64);
+  ldg256(b, entry + part * 64 + 32);
+  r.scale = __ldg(reinterpret_cast<const uint2*>(entry + kKvScaleOff + part * 8));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r.code[i] = a[i];
+    r.code[8 + i] = b[i];
+  }
+}
+__device__ __forceinline__ void zero_latent(RawLatent& r) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r.code[i] = 0u;
+  r.scale = make_uint2(0u, 0u);
+}
+// Scales of dimensions 32 s .. + 15 and + 16 .. + 31 as fp16 pairs.
+__device__ __forceinline__ void scale_pairs(const RawLatent& r, int s, __half2& lo, __half2& hi) {
+  const uint32_t w = (s < 2 ? r.scale.x : r.scale.y) >> (16 * (s & 1));
+  const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3));
+  lo = __low2half2(sc);
+  hi = __high2half2(sc);
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const AttendParams p, const PairGrid g) {
+  extern __shared__ __align__(1024) uint8_t pair_smem[];
+  uint8_t* smem = pair_smem;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + kOffQ, sK = sbase + kOffK, sV = sbase + kOffV, sP = sbase + kOffP;
+  volatile int* s_ring = reinterpret_cast<volatile int*>(smem + kOffRing);
+  volatile int* s_meta = reinterpret_cast<volatile int*>(smem + kOffMeta);
+  float* s_c = reinterpret_cast<float*>(smem + kOffC);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);
+  auto bar = [&](int i) { return sbase + kOffBars + 8 * i; };
+  constexpr uint32_t kTmemO = 0, kTmemS = 256;  // O: 2 x 128 columns, S: 2 x 64
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+
+  if (tid == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(kBarKF + i), 16);
+      mbar_init(bar(kBarKE + i), 1);
+      mbar_init(bar(kBarVF + i), 4);
+      mbar_init(bar(kBarVE + i), 1);
+    }
+    for (int i = 0; i < kPairRing; ++i) {
+      mbar_init(bar(kBarListed + i), 1);
+      mbar_init(bar(kBarTaken + i), rank == 0 ? 21 : 20);  // K, V and softmax warps, the MMA thread
+    }
+    mbar_init(bar(kBarS), 1);
+    mbar_init(bar(kBarS + 1), 1);
+    mbar_init(bar(kBarP), 8);
+    mbar_init(bar(kBarO), 1);
+    mbar_init(bar(kBarQF), 8);
+    mbar_init(bar(kBarQE), 1);
+    mbar_init(bar(kBarCF), 4);
+    mbar_init(bar(kBarCE), 4);
+    mbar_init(bar(kBarDrain), 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+
+  PairItem it{static_cast<int64_t>(blockIdx.x >> 1), 0, 0, 0, 0};
+  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, mbar_wait(bar(b), parity & 1u, s_abort, g.err)); };
+  // a tile's entry in the ring, for a warp that reads it
+  auto listed = [&](int i) { return wait(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
+  auto taken = [&](int i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarTaken + i % kPairRing));
+  };
+
+  if (warp >= kMma) {
+    regs_dec<kIssueRegs>();
+    if (warp == kList) {
+      // ------------------------------------------------------------- list
+      int base = 0;  // tiles of the items before
+      bool ok = true, bad = false;
+      auto open_tile = [&](int tile) {
+        return wait(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
+      };
+      auto publish = [&](int tile, int meta) {
+        if (lane == 0) s_meta[tile % kPairRing] = meta;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarListed + tile % kPairRing));
+      };
+      for (; ok && next_item(it, p, g, rank == 0 && lane == 0); it.k += gridDim.x >> 1) {
+        const int32_t* table = p.block_table + static_cast<int64_t>(it.seq) * p.max_blocks;
+        const int32_t* list = p.idx + it.t * p.n;
+        const int j_lo = static_cast<int>(static_cast<int64_t>(g.tiles) * it.split / g.splits) * kTile;
+        const int j_hi = static_cast<int>(
+            min(static_cast<int64_t>(p.n), static_cast<int64_t>(g.tiles) * (it.split + 1) / g.splits * kTile));
+        int pos[4], total = 0, opened = 0;  // keys packed, tiles opened; all but the last opened are published
+        auto fetch = [&](int j0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
+        };
+        fetch(j_lo);
+        for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
+          int slot[4];
+          slots_of(p, table, pos, slot, bad);
+          fetch(j0 + 128);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
+            if (m == 0) continue;
+            const int at = total + __popc(m & lanemask_lt());
+            total += __popc(m);
+            const bool open = total > opened * kTile;  // the batch's last key starts a tile
+            if (open && !(ok = open_tile(base + opened))) break;
+            if (slot[k] >= 0) s_ring[(base + at / kTile) % kPairRing * kTile + at % kTile] = slot[k];
+            __syncwarp();
+            if (open) {
+              if (opened > 0) publish(base + opened - 1, kTile | (opened == 1 ? kFirst : 0));
+              ++opened;
+            }
+          }
+        }
+        if (ok && opened == 0) {  // nothing listed: one tile without keys
+          ok = open_tile(base);
+          opened = 1;
+        }
+        if (ok) publish(base + opened - 1, (total - (opened - 1) * kTile) | (opened == 1 ? kFirst : 0) | kLast);
+        base += opened;
+      }
+      if (ok && open_tile(base)) publish(base, kStop);
+      if (__any_sync(~0u, bad) && rank == 0 && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
+    } else if (warp == kMma && rank == 0) {
+      // -------------------------------------------------------------- MMA
+      const uint32_t tmem = *s_tmem;
+      if (elect_one()) {
+        constexpr uint32_t kIdS = idesc_att(128, 128, 0, 0, 0), kIdR = idesc_att(128, 128, 1, 0, 0),
+                           kIdO = idesc_att(128, 256, 0, 0, 1);
+        const uint64_t dQ = smem_desc_sw128(sQ), dK = smem_desc_sw128(sK), dP = smem_desc_sw128(sP),
+                       dV = desc_mn_sw128(sV, kVBlk);
+        auto wait1 = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, s_abort, g.err); };
+        auto output = [&](int i, bool first) {  // O (+)= P V of tile i
+          if (!wait1(kBarP, i)) return false;
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u) {
+            if (!wait1(kBarVF + u, i)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint64_t a = dP + (((u >> 1) * kBlk + 32 * (2 * (u & 1) + kk)) >> 4);
+              const uint64_t b = dV + ((2 * u + kk) * 2048 >> 4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_pair(tmem + kTmemO + 128 * j, a, b + (2 * j * kVBlk >> 4), kIdO, !(first && u == 0 && kk == 0));
+            }
+            commit_pair(bar(kBarVE + u));
+          }
+          commit_pair(bar(kBarO));
+          return true;
+        };
+        bool ok = true, pending = false, prev_first = false;
+        int i = 0, n_items = 0;
+        for (; ok; ++i) {
+          if (!(ok = wait1(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)))) break;
+          const int meta = s_meta[i % kPairRing];
+          mbar_arrive(bar(kBarTaken + i % kPairRing));
+          if (meta & kStop) break;
+          const bool first = meta & kFirst;
+          if (first) {
+            // the last row's last product goes before the wait for this row's queries
+            if (pending && !(ok = output(i - 1, prev_first))) break;
+            pending = false;
+            if (!(ok = wait1(kBarQF, n_items++))) break;
+          }
+          const uint32_t d = tmem + kTmemS + 64 * (i & 1);
+#pragma unroll 1
+          for (int s = 0; s < 4; ++s) {
+            if (!(ok = wait1(kBarKF + s, i))) break;
+            tc_fence_after();
+            const uint32_t off = 2 * s * kBlk;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t o = (off + (k >> 2) * kBlk + 32 * (k & 3)) >> 4;
+              mma_pair(d, dQ + o, dK + o, kIdS, s > 0 || k > 0);
+            }
+            if (s == 0) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_pair(d, dQ + ((8 * kBlk + 32 * k) >> 4), dK + ((8 * kBlk + 32 * k) >> 4), kIdR, 1);
+            }
+            commit_pair(bar(kBarKE + s));
+          }
+          if (!ok) break;
+          commit_pair(bar(kBarS + (i & 1)));
+          if (meta & kLast) commit_pair(bar(kBarQE));
+          if (pending) ok = output(i - 1, prev_first);
+          pending = true;
+          prev_first = first;
+        }
+        if (ok && pending) output(i - 1, prev_first);
+        // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+        commit_pair(bar(kBarDrain));
+        int unused = 0;
+        mbar_wait(bar(kBarDrain), 0, &unused, g.err);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kQ) {
+    // ----------------------------------------------------------- queries
+    regs_inc<kQRegs>();
+    const int w = warp - kQ;
+    uint4 v[4][3];
+    bool ok = true;
+    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
+      const int h0 = it.hb * 2 * kHalf + rank * kHalf;
+      auto load = [&](int r0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) load_query_row(v[k], p, it.t, h0 + r0 + k, h0 + r0 + k < p.H, lane);
+      };
+      load(16 * w);
+      if (!(ok = wait(kBarQE, n + 1) && wait(kBarCE, n + 1))) break;
+#pragma unroll 1
+      for (int r0 = 16 * w;; r0 += 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          store_query_row(v[k], p.scale, smem + kOffQ, kBlk, r0 + k, s_c, lane, [](int s) { return s; });
+        if (r0 == 16 * w + 12) break;
+        load(r0 + 4);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kBarCF));
+        arrive_cluster(in_first(bar(kBarQF)));
+      }
+    }
+  } else if (warp >= kV) {
+    // ----------------------------------------------------------------- V
+    regs_dec<kVRegs>();
+    const int lw = warp - kV, key = lw * 16 + (lane & 15), half = lane >> 4, u = lw >> 1;
+    const uint32_t row = sV + 2 * half * kVBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
+    const uint32_t full = in_first(bar(kBarVF + u));
+    RawLatent raw;
+    int meta = 0;
+    auto take = [&](RawLatent& r, int& m, int i) {
+      if (!listed(i)) return false;
+      m = s_meta[i % kPairRing];
+      if (key < (m & 0xFFFF))
+        load_latent(r, p.kv + static_cast<int64_t>(s_ring[i % kPairRing * kTile + key]) * kKvEntry, 2 * rank + half);
+      else
+        zero_latent(r);
+      taken(i);
+      return true;
+    };
+    bool ok = take(raw, meta, 0);
+    for (int i = 0; ok && !(meta & kStop); ++i) {
+      RawLatent next;
+      int m = 0;
+      if (!(ok = take(next, m, i + 1)) || !(ok = wait(kBarVE + u, i + 1))) break;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        __half2 lo, hi;
+        scale_pairs(raw, s, lo, hi);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
+          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
+          sts128(row + (s >> 1) * kVBlk + (((4 * (s & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(full);
+      raw = next;
+      meta = m;
+    }
+  } else if (warp >= kK) {
+    // ----------------------------------------------------------------- K
+    const int lw = warp - kK, key = lw * 8 + (lane & 7), part = lane >> 3;
+    const uint32_t row = sK + (part >> 1) * kBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
+    const uint32_t full = in_first(bar(kBarKF));
+    RawLatent raw;
+    uint32_t rope[8];
+    int meta = 0;
+    auto take = [&](RawLatent& r, uint32_t (&ro)[8], int& m, int i) {
+      if (!listed(i)) return false;
+      m = s_meta[i % kPairRing];
+      const int k = rank * kHalf + key;
+      if (k < (m & 0xFFFF)) {
+        const uint8_t* e = p.kv + static_cast<int64_t>(s_ring[i % kPairRing * kTile + k]) * kKvEntry;
+        load_latent(r, e, part);
+        ldg256(ro, e + kKvRopeOff + part * 32);
+      } else {
+        zero_latent(r);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) ro[x] = 0u;
+      }
+      taken(i);
+      return true;
+    };
+    bool ok = take(raw, rope, meta, 0);
+    for (int i = 0; ok && !(meta & kStop); ++i) {
+      RawLatent next;
+      uint32_t next_rope[8];
+      int m = 0;
+      if (!(ok = take(next, next_rope, m, i + 1))) break;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (!(ok = wait(kBarKE + s, i + 1))) break;
+        if (s == 0) {
+          const uint32_t dst = sK + 8 * kBlk + key * 128;
+          sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);
+          sts128(dst + (((2 * part + 1) ^ sw) << 4), rope[4], rope[5], rope[6], rope[7]);
+        }
+        __half2 lo, hi;
+        scale_pairs(raw, s, lo, hi);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[4];
+          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
+          sts128(row + 2 * s * kBlk + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(full + 8 * s);
+      }
+      if (!ok) break;
+      raw = next;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) rope[x] = next_rope[x];
+      meta = m;
+    }
+  } else {
+    // ----------------------------------------------------------- softmax
+    regs_inc<kSoftRegs>();
+    const uint32_t tmem = *s_tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int row = tid & (kHalf - 1), part = tid >> 6;  // head; half of the keys and of the dimensions
+    const int bar_id = 1 + (warp & 1);
+    const uint32_t full = in_first(bar(kBarP));
+    const uint32_t p_row = sP + part * kBlk + row * 128, sw = static_cast<uint32_t>(row & 7);
+    // a word of this thread's and its partner's rows of P, while P is not in use
+    volatile float* mine = reinterpret_cast<volatile float*>(smem + kOffP + part * kBlk + row * 128);
+    volatile float* other = reinterpret_cast<volatile float*>(smem + kOffP + (part ^ 1) * kBlk + row * 128);
+    bool ok = true;
+    int i = 0;
+    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
+      float c = 0.f, m = INFINITY, l = 0.f;  // factor to log2 units, negated reference, sum
+      for (bool first = true, last = false; !last; first = false, ++i) {
+        int n_keys = 0;
+        if (listed(i)) {
+          const int meta = s_meta[i % kPairRing];
+          last = meta & kLast;
+          n_keys = (meta & 0xFFFF) - part * kHalf;  // of this thread's half
+          taken(i);
+        } else {
+          ok = false;
+        }
+        ok = wait(kBarS + (i & 1), static_cast<uint32_t>(i >> 1)) && ok;
+        if (first) {
+          ok = wait(kBarCF, n) && ok;
+          c = s_c[row];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarCE));
+        }
+        tc_fence_after();
+        float x[kHalf];
+        auto scores = [&] {  // x <- score - reference, -inf behind the last key; the largest
+          uint32_t (&u)[kHalf] = reinterpret_cast<uint32_t(&)[kHalf]>(x);
+          tmem_ld32(tmem + kTmemS + 64 * (i & 1), reinterpret_cast<uint32_t(&)[32]>(u[0]));
+          tmem_ld32(tmem + kTmemS + 64 * (i & 1) + 32, reinterpret_cast<uint32_t(&)[32]>(u[32]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kHalf; k += 2) {
+            const float2 a = __ffma2_rn(make_float2(x[k], x[k + 1]), make_float2(c, c), make_float2(m, m));
+            x[k] = a.x;
+            x[k + 1] = a.y;
+          }
+          if (n_keys < kHalf) {
+#pragma unroll
+            for (int k = 0; k < kHalf; ++k)
+              if (k >= n_keys) x[k] = -INFINITY;
+          }
+          float mx = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int k = 2; k < kHalf; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+          return mx;
+        };
+        const float mx = scores();
+        // the same decision in both warps of these heads; a wait that gave up goes this way too
+        const bool moved = heads_bar_or(bar_id, !ok || mx > kRise);
+        if (moved) {
+          if (!first) ok = wait(kBarO, i - 1) && ok;
+          if (heads_bar_or(bar_id, !ok)) {
+            ok = false;
+            ++i;
+            break;
+          }
+          tc_fence_after();
+          // largest score itself: m may have been infinite
+          float top = -INFINITY;
+          tmem_ld32(tmem + kTmemS + 64 * (i & 1), reinterpret_cast<uint32_t(&)[32]>(x[0]));
+          tmem_ld32(tmem + kTmemS + 64 * (i & 1) + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < kHalf; ++k)
+            if (k < n_keys) top = fmaxf(top, x[k] * c);
+          *mine = top;
+          named_bar_sync(bar_id, 64);
+          top = fmaxf(fmaxf(top, *other), -m);
+          const float f = top == -INFINITY ? 1.f : ex2(-m - top);
+          m = -top;
+          l *= f;
+          named_bar_sync(bar_id, 64);
+          if (!first) {
+#pragma unroll 1
+            for (int q = 0; q < 256; q += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem + kTmemO + q, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(tmem + kTmemO + q, o);
+            }
+            tmem_wait_st();
+          }
+          scores();
+        }
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t w[kHalf / 2];
+#pragma unroll
+        for (int k = 0; k < kHalf; k += 2) {
+          const float2 a = make_float2(ex2(x[k]), ex2(x[k + 1]));
+          sum = __fadd2_rn(sum, a);
+          const __half2 h = __floats2half2_rn(a.x, a.y);
+          w[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        l += sum.x + sum.y;
+        // P of the last tile is consumed (checked above when the reference moved, at the end of the last row)
+        if (!moved && !first) ok = wait(kBarO, i - 1) && ok;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sts128(p_row + ((k ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(full);
+      }
+      // ---------------------------------------------------------- output
+      ok = ok && wait(kBarO, i - 1);
+      if (heads_bar_or(bar_id, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      *mine = l;
+      named_bar_sync(bar_id, 64);
+      l += *other;
+      named_bar_sync(bar_id, 64);
+      const int h = it.hb * 2 * kHalf + rank * kHalf + row;
+      const int64_t part_row = it.k * 2 * kHalf + rank * kHalf + row;
+      const float f = g.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      if (part == 0 && h < p.H) {
+        if (g.splits > 1)
+          g.part_ml[part_row] = make_float2(-m, l);
+        else if (p.lse)
+          p.lse[it.t * p.H + h] = l == 0.f ? -INFINITY : (log2f(l) - m) * kLn2;
+      }
+#pragma unroll 1
+      for (int q = 0; q < 8; ++q) {  // 32 dimensions
+        uint32_t o[32];
+        tmem_ld32(tmem + kTmemO + 32 * q, o);
+        tmem_wait_ld();
+        const int dim = 256 * part + 32 * q;
+        if (h >= p.H) {
+          // no such head
+        } else if (g.splits > 1) {
+          uint4* dst = reinterpret_cast<uint4*>(g.part_o + part_row * kKvLat + dim);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          uint32_t b[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 y =
+                __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
+            b[k] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (it.t * p.H + h) * kKvLat + dim);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
+  }
+  // a block's memory and barriers are in use until its partner is done too
+  __syncwarp();
+  cluster_sync();
+  if (warp == kMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(*s_tmem) : "memory");
+  }
+}
+
+// Joins the splits of one (row, head): out = sum_s 2^(m_s - m) O_s / sum_s
+// 2^(m_s - m) l_s.
+__global__ void __launch_bounds__(128) attend_pair_join_kernel(const AttendParams p, const PairGrid g) {
+  const int64_t t = blockIdx.x / p.H;
+  const int h = static_cast<int>(blockIdx.x % p.H);
+  const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
+  if (seq < 0 || seq >= p.B) return;
+  const int64_t row0 = (t * g.head_blocks + h / kTile) * g.splits * kTile + h % kTile;
+  float m = -INFINITY;
+  for (int s = 0; s < g.splits; ++s) m = fmaxf(m, g.part_ml[row0 + s * kTile].x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < g.splits; ++s) {
+    const float2 ml = g.part_ml[row0 + s * kTile];
+    const float w = ex2(ml.x - ref);
+    const float4 o = reinterpret_cast<const float4*>(g.part_o + (row0 + s * kTile) * kKvLat)[threadIdx.x];
+    sum = fmaf(w, ml.y, sum);
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(p.out + (t * p.H + h) * kKvLat)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (p.lse && threadIdx.x == 0) p.lse[t * p.H + h] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+}
+
+struct PairPlan {
+  int head_blocks, splits, tiles;
+  int64_t items;
+  size_t off_o, bytes;
+};
+
+PairPlan plan_pair(int64_t T, int H, int n, int sms) {
+  PairPlan P{};
+  P.head_blocks = (H + 2 * kHalf - 1) / (2 * kHalf);
+  P.tiles = (n + kTile - 1) / kTile;
+  const int64_t rows = T * P.head_blocks, clusters = std::max(sms / 2, 1);
+  P.splits = rows >= clusters || rows == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / rows, P.tiles));
+  P.items = rows * P.splits;
+  P.bytes = 256;
+  if (P.splits > 1) {
+    const size_t part_rows = static_cast<size_t>(P.items) * 2 * kHalf;
+    P.off_o = (256 + part_rows * sizeof(float2) + 255) / 256 * 256;
+    P.bytes = P.off_o + part_rows * kKvLat * sizeof(float);
+  }
+  return P;
+}
+
+}  // namespace
+
+size_t attend_pair_workspace_bytes(int64_t T, int H, int n, int sms) { return plan_pair(T, H, n, sms).bytes; }
+
+cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int sms, cudaStream_t st) {
+  const PairPlan P = plan_pair(p.T, p.H, p.n, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PairGrid g{P.head_blocks, P.splits, P.tiles, P.items, reinterpret_cast<float*>(ws + P.off_o),
+             reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
+  cudaError_t e = cudaFuncSetAttribute(attend_kv4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(P.items, std::max(sms / 2, 1))));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attend_kv4_pair_kernel, p, g);
+  if (e != cudaSuccess || P.splits == 1) return e;
+  attend_pair_join_kernel<<<static_cast<unsigned>(p.T * p.H), 128, 0, st>>>(p, g);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

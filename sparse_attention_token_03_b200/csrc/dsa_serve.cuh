@@ -104,5 +104,8 @@ struct AttendParams {
 };
 size_t attend_workspace_bytes(int64_t T, int H, int n, int sms);
 cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st);
+// More than 64 heads (launch_attend_kv4 and attend_workspace_bytes choose).
+size_t attend_pair_workspace_bytes(int64_t T, int H, int n, int sms);
+cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int sms, cudaStream_t st);
 
 }  // namespace dsa
