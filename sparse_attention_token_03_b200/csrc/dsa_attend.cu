@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       int total = 0;  // keys packed; total / kKt tiles are published
       bool ok = true, bad = false;
       auto open_tile = [&](int tile) {  // before the first write to a ring tile
-        return __all_sync(~0u, mbar_wait(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
+        return __all_sync(~0u, wait_bar(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
       };
       auto publish = [&](int tile, int count) {
         if (lane == 0) s_ring_n[tile % kRing] = count;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         bool ok = true;
         auto output = [&](int i) {  // O^T += V^T P^T of tile i
           const int b = i & 1;
-          if (!mbar_wait(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
+          if (!wait_bar(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
           tc_fence_after();
 #pragma unroll 1  // 4 x 4 MMAs: unrolled, their descriptors spill
           for (int s = 0; s < kParts; ++s) {
@@ -360,10 +360,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         for (; ok; ++i) {
           const int b = i & 1;
           const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
-          if (!(ok = mbar_wait(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
+          if (!(ok = wait_bar(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
 #pragma unroll 1
           for (int s = 0; s < kParts; ++s) {
-            if (s > 0 && !(ok = mbar_wait(bar_full(b, s), ph, s_abort, g.err))) break;
+            if (s > 0 && !(ok = wait_bar(bar_full(b, s), ph, s_abort, g.err))) break;
             tc_fence_after();
             const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
 #pragma unroll
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
         mma_commit(bar_drain);
         int unused = 0;
-        mbar_wait(bar_drain, 0, &unused, g.err);
+        wait_bar(bar_drain, 0, &unused, g.err);
       }
       __syncwarp();
     }
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     int n_keys = 0;
     auto take = [&](RawKey& r, int& count, int tile) {  // a tile's loads, once its slots are listed
       const int k = tile % kRing;
-      if (!__all_sync(~0u, mbar_wait(bar_listed(k), static_cast<uint32_t>(tile / kRing) & 1u, s_abort, g.err))) return false;
+      if (!__all_sync(~0u, wait_bar(bar_listed(k), static_cast<uint32_t>(tile / kRing) & 1u, s_abort, g.err))) return false;
       count = s_ring_n[k];
       load_raw(r, p.kv, s_ring[k * kKt + key], key < count, part, group);
       __syncwarp();
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 #pragma unroll
       for (int u = 0; u < kParts / 2; ++u) {
         const int s = 2 * u + group;
-        if (!(ok = __all_sync(~0u, mbar_wait(bar_empty(b, s), ph, s_abort, g.err)))) break;
+        if (!(ok = __all_sync(~0u, wait_bar(bar_empty(b, s), ph, s_abort, g.err)))) break;
         if (u == 0) {
           if (warp == kSoftWarps && lane == 0) s_n[b] = n_keys;
           sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
@@ -514,10 +514,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     int nt = 0;  // tiles
     for (int i = 0;; nt = ++i) {
       const int b = i & 1;
-      ok = __all_sync(~0u, mbar_wait(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+      ok = __all_sync(~0u, wait_bar(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const int n_keys = ok ? s_n[b] : 0;
       if (n_keys > 0)
-        ok = __all_sync(~0u, mbar_wait(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
+        ok = __all_sync(~0u, wait_bar(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const bool end = !ok || n_keys == 0;
       bool rise = end;
       float x[NH / 2];
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       // the same decision in all four warps; the end of the list and a wait that gave up go this way too
       const bool moved = soft_bar_or(rise);
       if (moved) {
-        if (i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+        if (i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
         if (soft_bar_or(end || !ok)) break;
         tc_fence_after();
         {
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hd);
       }
       // P of the last tile is consumed (checked above when the reference moved)
-      if (!moved && i > 0) ok = __all_sync(~0u, mbar_wait(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+      if (!moved && i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         sts32(p0 + ((j ^ r0) << 4), w[2 * j]);

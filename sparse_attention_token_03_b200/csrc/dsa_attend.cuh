@@ -15,6 +15,26 @@ namespace dsa {
 constexpr float kRise = 8.f;  // log2 of the largest P before the reference moves
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
+// mbar_wait in fewer instructions (the roles of these kernels wait at some
+// thirty places, and their loops share one instruction cache): the clock is
+// read and the abort flag looked at after every 256 tries.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n & 255u) continue;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag) return false;
+    if (now - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
   // M- or N-major operand: rows of 64 consecutive M (N) elements, 8 K rows per
   // 1024-byte atom; mn_stride between 64-element groups, 1024 between K groups

@@ -74,7 +74,7 @@ constexpr int kFirst = 1 << 16, kLast = 1 << 17, kStop = 1 << 18;
 
 struct PairGrid {
   int head_blocks, splits, tiles;  // tiles: of a whole list
-  int64_t items;                   // T * head_blocks * splits
+  uint32_t items;                  // T * head_blocks * splits, below 2^31
   float* part_o;                   // [items][128][512]
   float2* part_ml;                 // [items][128]
   uint32_t* err;
@@ -82,14 +82,16 @@ struct PairGrid {
 
 // A cluster's next item with a row to work on: item k and what it stands for.
 struct PairItem {
-  int64_t k, t;
+  uint32_t k;
+  int64_t t;
   int hb, split, seq;
 };
 __device__ __forceinline__ bool next_item(PairItem& it, const AttendParams& p, const PairGrid& g, bool report) {
   for (; it.k < g.items; it.k += gridDim.x >> 1) {
-    it.split = static_cast<int>(it.k % g.splits);
-    it.hb = static_cast<int>(it.k / g.splits % g.head_blocks);
-    it.t = it.k / g.splits / g.head_blocks;
+    const uint32_t row = it.k / static_cast<uint32_t>(g.splits);
+    it.split = static_cast<int>(it.k - row * g.splits);
+    it.t = row / static_cast<uint32_t>(g.head_blocks);
+    it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
     it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
     if (it.seq >= 0 && it.seq < p.B) return true;
     if (it.seq >= p.B && report && p.status) atomicOr(p.status, kErrOverflow);  // else padding
@@ -223,8 +225,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   cluster_sync();
   tc_fence_after();
 
-  PairItem it{static_cast<int64_t>(blockIdx.x >> 1), 0, 0, 0, 0};
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, mbar_wait(bar(b), parity & 1u, s_abort, g.err)); };
+  PairItem it{blockIdx.x >> 1, 0, 0, 0, 0};
+  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort, g.err)); };
   // a tile's entry in the ring, for a warp that reads it
   auto listed = [&](int i) { return wait(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
   auto taken = [&](int i) {
@@ -262,15 +264,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
           int slot[4];
           slots_of(p, table, pos, slot, bad);
           fetch(j0 + 128);
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 4; ++k) {
-            const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
+            const int mine = slot[0];
+            slot[0] = slot[1];
+            slot[1] = slot[2];
+            slot[2] = slot[3];
+            const uint32_t m = __ballot_sync(~0u, mine >= 0);
             if (m == 0) continue;
             const int at = total + __popc(m & lanemask_lt());
             total += __popc(m);
             const bool open = total > opened * kTile;  // the batch's last key starts a tile
             if (open && !(ok = open_tile(base + opened))) break;
-            if (slot[k] >= 0) s_ring[(base + at / kTile) % kPairRing * kTile + at % kTile] = slot[k];
+            if (mine >= 0) s_ring[(base + at / kTile) % kPairRing * kTile + at % kTile] = mine;
             __syncwarp();
             if (open) {
               if (opened > 0) publish(base + opened - 1, kTile | (opened == 1 ? kFirst : 0));
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
                            kIdO = idesc_att(128, 256, 0, 0, 1);
         const uint64_t dQ = smem_desc_sw128(sQ), dK = smem_desc_sw128(sK), dP = smem_desc_sw128(sP),
                        dV = desc_mn_sw128(sV, kVBlk);
-        auto wait1 = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, s_abort, g.err); };
+        auto wait1 = [&](int b, uint32_t parity) { return wait_bar(bar(b), parity & 1u, s_abort, g.err); };
         auto output = [&](int i, bool first) {  // O (+)= P V of tile i
           if (!wait1(kBarP, i)) return false;
 #pragma unroll 1
@@ -357,7 +363,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
         commit_pair(bar(kBarDrain));
         int unused = 0;
-        mbar_wait(bar(kBarDrain), 0, &unused, g.err);
+        wait_bar(bar(kBarDrain), 0, &unused, g.err);
       }
       __syncwarp();
     }
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     bool ok = true;
     int i = 0;
     for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
-      float c = 0.f, m = INFINITY, l = 0.f;  // factor to log2 units, negated reference, sum
+      float c = 0.f, m = 0.f, l = 0.f;  // factor to log2 units, negated reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         int n_keys = 0;
         if (listed(i)) {
@@ -520,7 +526,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         }
         tc_fence_after();
         float x[kHalf];
-        auto scores = [&] {  // x <- score - reference, -inf behind the last key; the largest
+        bool moved = false;
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          // x <- score - reference, -inf behind the last key; mx: the largest
           uint32_t (&u)[kHalf] = reinterpret_cast<uint32_t(&)[kHalf]>(x);
           tmem_ld32(tmem + kTmemS + 64 * (i & 1), reinterpret_cast<uint32_t(&)[32]>(u[0]));
           tmem_ld32(tmem + kTmemS + 64 * (i & 1) + 32, reinterpret_cast<uint32_t(&)[32]>(u[32]));
@@ -536,34 +545,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
             for (int k = 0; k < kHalf; ++k)
               if (k >= n_keys) x[k] = -INFINITY;
           }
+          if (pass > 0) break;
           float mx = fmaxf(x[0], x[1]);
 #pragma unroll
           for (int k = 2; k < kHalf; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
-          return mx;
-        };
-        const float mx = scores();
-        // the same decision in both warps of these heads; a wait that gave up goes this way too
-        const bool moved = heads_bar_or(bar_id, !ok || mx > kRise);
-        if (moved) {
+          // the same decision in both warps of these heads; a wait that gave up goes this way too
+          moved = heads_bar_or(bar_id, !ok || first || mx > kRise);
+          if (!moved) break;
           if (!first) ok = wait(kBarO, i - 1) && ok;
           if (heads_bar_or(bar_id, !ok)) {
             ok = false;
-            ++i;
             break;
           }
           tc_fence_after();
-          // largest score itself: m may have been infinite
-          float top = -INFINITY;
-          tmem_ld32(tmem + kTmemS + 64 * (i & 1), reinterpret_cast<uint32_t(&)[32]>(x[0]));
-          tmem_ld32(tmem + kTmemS + 64 * (i & 1) + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < kHalf; ++k)
-            if (k < n_keys) top = fmaxf(top, x[k] * c);
-          *mine = top;
+          *mine = mx - m;
           named_bar_sync(bar_id, 64);
-          top = fmaxf(fmaxf(top, *other), -m);
-          const float f = top == -INFINITY ? 1.f : ex2(-m - top);
+          float top = fmaxf(mx - m, *other);
+          if (!first) top = fmaxf(top, -m);
+          if (top == -INFINITY) top = 0.f;  // no keys so far
+          const float f = first ? 1.f : ex2(-m - top);
           m = -top;
           l *= f;
           named_bar_sync(bar_id, 64);
@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
             }
             tmem_wait_st();
           }
-          scores();
         }
+        if (moved && !ok) break;  // decided by both warps
         float2 sum = make_float2(0.f, 0.f);
         uint32_t w[kHalf / 2];
 #pragma unroll
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       l += *other;
       named_bar_sync(bar_id, 64);
       const int h = it.hb * 2 * kHalf + rank * kHalf + row;
-      const int64_t part_row = it.k * 2 * kHalf + rank * kHalf + row;
+      const int64_t part_row = static_cast<int64_t>(it.k) * 2 * kHalf + rank * kHalf + row;
       const float f = g.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       if (part == 0 && h < p.H) {
         if (g.splits > 1)
@@ -719,7 +719,7 @@ size_t attend_pair_workspace_bytes(int64_t T, int H, int n, int sms) { return pl
 cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int sms, cudaStream_t st) {
   const PairPlan P = plan_pair(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  PairGrid g{P.head_blocks, P.splits, P.tiles, P.items, reinterpret_cast<float*>(ws + P.off_o),
+  PairGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(P.items), reinterpret_cast<float*>(ws + P.off_o),
              reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e != cudaSuccess) return e;
