@@ -97,6 +97,7 @@ struct AttGrid {
   float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
   float2* part_ml;                 // [T][head_blocks][splits][NH]
   uint32_t* err;
+  PageDiv div;
 };
 
 // 16 lanes x NH columns of fp32: thread i holds rows i / 4 (values 4j, 4j + 1)
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       fetch(j_lo);
       for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
         int slot[4];
-          slots_of(p, table, pos, slot, bad);
+        slots_of(p, g.div, table, pos, slot, bad);
         fetch(j0 + 128);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -776,7 +777,7 @@ cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, c
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float4*>(ws + P.off_o),
-            reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
+            reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
   return P.NH == 16 ? launch_nh<16>(p, g, st) : P.NH == 32 ? launch_nh<32>(p, g, st) : launch_nh<64>(p, g, st);
 }
 

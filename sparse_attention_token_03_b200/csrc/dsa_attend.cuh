@@ -35,6 +35,42 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
   return true;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Waits until bit `which` of `ready` is set, bit j telling that lane j's
+// barrier (if `has`) has passed its phase.  A look at a barrier takes some 300
+// cycles while the tensor core reads shared memory, so a warp that needs
+// several in turn looks at all of them at once and only again for those that
+// were not ready.
+__device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
+                                         volatile int* abort_flag, uint32_t* err) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !((ready >> which) & 1u); ++n) {
+    ready = __ballot_sync(~0u, has && mbar_test(bar, parity));
+    if (n & 255u) continue;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) t0 = now;
+    bool stop = *abort_flag != 0;
+    if (now - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicOr(err, kErrTimeout);
+      stop = true;
+    }
+    if (__any_sync(~0u, stop)) return false;
+  }
+  return true;
+}
+
 __device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t mn_stride) {
   // M- or N-major operand: rows of 64 consecutive M (N) elements, 8 K rows per
   // 1024-byte atom; mn_stride between 64-element groups, 1024 between K groups
@@ -91,15 +127,27 @@ __device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
       : "l"(p));
 }
 
+// Division of a position (below 2^31) by the page size as a product: with s =
+// ceil(log2 d) and mul = ceil(2^(31 + s) / d) the product's error n (mul d -
+// 2^(31 + s)) / (d 2^(31 + s)) is below 1 / d, so the quotient is exact.
+struct PageDiv {
+  uint32_t mul, shift;
+};
+inline PageDiv page_div(int d) {
+  uint32_t s = 0;
+  while ((int64_t(1) << s) < d) ++s;
+  return {static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 // Pool rows of four list entries of a sequence (its block table `table`), or -1
 // where nothing is listed or the position or page is outside its range, which
 // sets `bad`.  The four table loads are in flight together.
-__device__ __forceinline__ void slots_of(const AttendParams& p, const int32_t* table, const int (&pos)[4], int (&slot)[4],
+__device__ __forceinline__ void slots_of(const AttendParams& p, PageDiv div, const int32_t* table, const int (&pos)[4], int (&slot)[4],
                                          bool& bad) {
   int blk[4], page[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    blk[k] = static_cast<int>(static_cast<uint32_t>(max(pos[k], 0)) / static_cast<uint32_t>(p.page_size));
+    blk[k] = static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(max(pos[k], 0))) * div.mul >> div.shift);
     page[k] = __ldg(table + min(blk[k], p.max_blocks - 1));
   }
 #pragma unroll

@@ -46,7 +46,7 @@ constexpr int kTile = 128, kHalf = 64;            // keys of a tile; keys of K a
 constexpr uint32_t kBlk = kHalf * 128;            // a 64-column block of K, Q or P
 constexpr uint32_t kVBlk = kTile * 128;           // a 64-column block of V
 constexpr int kNBlk = kKvQ / 64;
-constexpr int kK = 4, kV = 12, kQ = 20, kMma = 24, kList = 25;  // first warps of the roles, softmax from 0
+constexpr int kK = 4, kV = 12, kQ = 20, kMma = 24, kList = 25, kMmaO = 26;  // first warps of the roles, softmax from 0
 constexpr int kPairThreads = 28 * 32;
 constexpr int kPairRing = 4;                      // tiles that the list warp may be ahead
 // registers per thread: 72 at launch, then shared out by warpgroup
@@ -60,11 +60,11 @@ constexpr uint32_t kOffMeta = kOffRing + kPairRing * kTile * 4;  // keys and fla
 constexpr uint32_t kOffC = kOffMeta + kPairRing * 4;             // per head: factor of a score in log2 units
 constexpr uint32_t kOffBars = kOffC + kHalf * 4;
 // barriers: K full, K empty, V full, V empty [4 parts each], listed, taken
-// [ring], scores [2], then P full, output done, Q full, Q empty, factors full,
-// factors empty, drain
+// [ring], scores [2], scores read [2], then P full, output done, Q full, Q empty, factors full,
+// factors empty, drain [2]
 constexpr int kBarKF = 0, kBarKE = 4, kBarVF = 8, kBarVE = 12, kBarListed = 16, kBarTaken = kBarListed + kPairRing,
-              kBarS = kBarTaken + kPairRing, kBarP = kBarS + 2, kBarO = kBarP + 1, kBarQF = kBarO + 1, kBarQE = kBarQF + 1,
-              kBarCF = kBarQE + 1, kBarCE = kBarCF + 1, kBarDrain = kBarCE + 1, kBars = kBarDrain + 1;
+              kBarS = kBarTaken + kPairRing, kBarSE = kBarS + 2, kBarP = kBarSE + 2, kBarO = kBarP + 1, kBarQF = kBarO + 1, kBarQE = kBarQF + 1,
+              kBarCF = kBarQE + 1, kBarCE = kBarCF + 1, kBarDrain = kBarCE + 1, kBars = kBarDrain + 2;
 constexpr uint32_t kOffMisc = kOffBars + 8 * kBars;
 constexpr uint32_t kPairSmem = kOffMisc + 16;
 static_assert(kOffBars % 8 == 0 && kPairSmem <= 227u * 1024u, "shared memory layout");
@@ -78,6 +78,7 @@ struct PairGrid {
   float* part_o;                   // [items][128][512]
   float2* part_ml;                 // [items][128]
   uint32_t* err;
+  PageDiv div;
 };
 
 // A cluster's next item with a row to work on: item k and what it stands for.
@@ -151,13 +152,13 @@ __device__ __forceinline__ bool heads_bar_or(int id, bool v) {
 // 128 latent dimensions of a key: 64 bytes of codes and eight scales.
 struct RawLatent {
   uint32_t code[16];
-  uint2 scale;
+  uint64_t scale;
 };
 __device__ __forceinline__ void load_latent(RawLatent& r, const uint8_t* entry, int part) {
   uint32_t a[8], b[8];
   ldg256(a, entry + part * 64);
   ldg256(b, entry + part * 64 + 32);
-  r.scale = __ldg(reinterpret_cast<const uint2*>(entry + kKvScaleOff + part * 8));
+  r.scale = __ldg(reinterpret_cast<const unsigned long long*>(entry + kKvScaleOff + part * 8));
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     r.code[i] = a[i];
@@ -167,14 +168,25 @@ __device__ __forceinline__ void load_latent(RawLatent& r, const uint8_t* entry, 
 __device__ __forceinline__ void zero_latent(RawLatent& r) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) r.code[i] = 0u;
-  r.scale = make_uint2(0u, 0u);
+  r.scale = 0u;
 }
-// Scales of dimensions 32 s .. + 15 and + 16 .. + 31 as fp16 pairs.
-__device__ __forceinline__ void scale_pairs(const RawLatent& r, int s, __half2& lo, __half2& hi) {
-  const uint32_t w = (s < 2 ? r.scale.x : r.scale.y) >> (16 * (s & 1));
-  const __half2 sc = __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3));
-  lo = __low2half2(sc);
-  hi = __high2half2(sc);
+// Decodes the next 32 dimensions to four chunks of 16 bytes, chunk k at dst +
+// ((k ^ swz) << 4), and moves the rest down (a loop over all 128 keeps the
+// code small, which counts here: the roles' loops together pass the size of
+// the instruction cache).
+__device__ __forceinline__ void decode_step(RawLatent& r, uint32_t dst, uint32_t swz) {
+  const __half2 sc =
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(r.scale & 0xFFFFu), __NV_E4M3));
+  const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t o[4];
+    decode8(r.code[k], k < 2 ? lo : hi, o);
+    sts128(dst + ((k ^ swz) << 4), o[0], o[1], o[2], o[3]);
+  }
+  r.scale >>= 16;
+#pragma unroll
+  for (int k = 0; k < 12; ++k) r.code[k] = r.code[k + 4];
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const AttendParams p, const PairGrid g) {
@@ -202,10 +214,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     }
     for (int i = 0; i < kPairRing; ++i) {
       mbar_init(bar(kBarListed + i), 1);
-      mbar_init(bar(kBarTaken + i), rank == 0 ? 21 : 20);  // K, V and softmax warps, the MMA thread
+      mbar_init(bar(kBarTaken + i), rank == 0 ? 22 : 20);  // K, V and softmax warps, the MMA warps
     }
     mbar_init(bar(kBarS), 1);
     mbar_init(bar(kBarS + 1), 1);
+    mbar_init(bar(kBarSE), 8);
+    mbar_init(bar(kBarSE + 1), 8);
     mbar_init(bar(kBarP), 8);
     mbar_init(bar(kBarO), 1);
     mbar_init(bar(kBarQF), 8);
@@ -213,6 +227,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     mbar_init(bar(kBarCF), 4);
     mbar_init(bar(kBarCE), 4);
     mbar_init(bar(kBarDrain), 1);
+    mbar_init(bar(kBarDrain + 1), 1);
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -238,108 +253,86 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     regs_dec<kIssueRegs>();
     if (warp == kList) {
       // ------------------------------------------------------------- list
-      int base = 0;  // tiles of the items before
-      bool ok = true, bad = false;
-      auto open_tile = [&](int tile) {
-        return wait(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
-      };
-      auto publish = [&](int tile, int meta) {
-        if (lane == 0) s_meta[tile % kPairRing] = meta;
+      int tile = 0, keys = 0;  // the open tile, and how many keys it has
+      bool ok = true, bad = false, first = true;
+      auto publish = [&](int flags) {  // the open tile
+        if (lane == 0) s_meta[tile % kPairRing] = keys | flags;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarListed + tile % kPairRing));
       };
-      for (; ok && next_item(it, p, g, rank == 0 && lane == 0); it.k += gridDim.x >> 1) {
-        const int32_t* table = p.block_table + static_cast<int64_t>(it.seq) * p.max_blocks;
-        const int32_t* list = p.idx + it.t * p.n;
-        const int j_lo = static_cast<int>(static_cast<int64_t>(g.tiles) * it.split / g.splits) * kTile;
-        const int j_hi = static_cast<int>(
-            min(static_cast<int64_t>(p.n), static_cast<int64_t>(g.tiles) * (it.split + 1) / g.splits * kTile));
-        int pos[4], total = 0, opened = 0;  // keys packed, tiles opened; all but the last opened are published
-        auto fetch = [&](int j0) {
+      auto turn = [&](int flags) {  // publishes the open tile and opens the next one
+        publish(flags);
+        ++tile;
+        keys = 0;
+        ok = wait(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
+      };
+      int j0 = 0, j_hi = 0;  // the item's entries that are left
+      const int32_t *table = nullptr, *list = nullptr;
+      int pos[4];
+      auto fetch = [&] {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
-        };
-        fetch(j_lo);
-        for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
-          int slot[4];
-          slots_of(p, table, pos, slot, bad);
-          fetch(j0 + 128);
+        for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
+        j0 += 128;
+      };
+      while (ok && next_item(it, p, g, rank == 0 && lane == 0)) {
+        table = p.block_table + static_cast<int64_t>(it.seq) * p.max_blocks;
+        list = p.idx + it.t * p.n;
+        // below 2^23 tiles and 2^8 splits
+        j0 = static_cast<int>(static_cast<uint32_t>(g.tiles) * it.split / static_cast<uint32_t>(g.splits)) * kTile;
+        j_hi = min(p.n, static_cast<int>(static_cast<uint32_t>(g.tiles) * (it.split + 1) / static_cast<uint32_t>(g.splits)) * kTile);
+        first = true;
+        fetch();
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            const int mine = slot[0];
+        for (int left = (j_hi - j0 + 255) >> 7; left > 0 && ok; --left) {  // steps of 128 entries
+          int slot[4];
+          slots_of(p, g.div, table, pos, slot, bad);
+          fetch();
+#pragma unroll 1
+          for (int k = 0; k < 4 && ok; ++k) {
+            int mine = slot[0];
             slot[0] = slot[1];
             slot[1] = slot[2];
             slot[2] = slot[3];
             const uint32_t m = __ballot_sync(~0u, mine >= 0);
-            if (m == 0) continue;
-            const int at = total + __popc(m & lanemask_lt());
-            total += __popc(m);
-            const bool open = total > opened * kTile;  // the batch's last key starts a tile
-            if (open && !(ok = open_tile(base + opened))) break;
-            if (mine >= 0) s_ring[(base + at / kTile) % kPairRing * kTile + at % kTile] = mine;
-            __syncwarp();
-            if (open) {
-              if (opened > 0) publish(base + opened - 1, kTile | (opened == 1 ? kFirst : 0));
-              ++opened;
+            int at = keys + __popc(m & lanemask_lt());
+            if (mine >= 0 && at < kTile) s_ring[tile % kPairRing * kTile + at] = mine;
+            keys += __popc(m);
+            if (keys > kTile) {  // the rest starts the next tile, so this one is not the last
+              const int rest = keys - kTile;
+              keys = kTile;
+              turn(first ? kFirst : 0);
+              first = false;
+              if (mine >= 0 && at >= kTile) s_ring[tile % kPairRing * kTile + at - kTile] = mine;
+              keys = rest;
             }
           }
         }
-        if (ok && opened == 0) {  // nothing listed: one tile without keys
-          ok = open_tile(base);
-          opened = 1;
-        }
-        if (ok) publish(base + opened - 1, (total - (opened - 1) * kTile) | (opened == 1 ? kFirst : 0) | kLast);
-        base += opened;
+        it.k += gridDim.x >> 1;
+        if (ok) turn(kLast | (first ? kFirst : 0));  // without keys where nothing is listed
       }
-      if (ok && open_tile(base)) publish(base, kStop);
+      if (ok) publish(kStop);
       if (__any_sync(~0u, bad) && rank == 0 && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
     } else if (warp == kMma && rank == 0) {
-      // -------------------------------------------------------------- MMA
+      // -------------------------------------------------- MMAs of the scores
       const uint32_t tmem = *s_tmem;
-      if (elect_one()) {
-        constexpr uint32_t kIdS = idesc_att(128, 128, 0, 0, 0), kIdR = idesc_att(128, 128, 1, 0, 0),
-                           kIdO = idesc_att(128, 256, 0, 0, 1);
-        const uint64_t dQ = smem_desc_sw128(sQ), dK = smem_desc_sw128(sK), dP = smem_desc_sw128(sP),
-                       dV = desc_mn_sw128(sV, kVBlk);
-        auto wait1 = [&](int b, uint32_t parity) { return wait_bar(bar(b), parity & 1u, s_abort, g.err); };
-        auto output = [&](int i, bool first) {  // O (+)= P V of tile i
-          if (!wait1(kBarP, i)) return false;
+      constexpr uint32_t kIdS = idesc_att(128, 128, 0, 0, 0), kIdR = idesc_att(128, 128, 1, 0, 0);
+      const uint64_t dQ = smem_desc_sw128(sQ), dK = smem_desc_sw128(sK);
+      bool ok = true;
+      int n_items = 0;
+      for (int i = 0;; ++i) {
+        if (!listed(i)) break;
+        const int meta = s_meta[i % kPairRing];
+        taken(i);
+        if (meta & kStop) break;
+        if ((meta & kFirst) && !wait(kBarQF, n_items++)) break;
+        if (!wait(kBarSE + (i & 1), static_cast<uint32_t>(i >> 1) + 1u)) break;  // scores of tile i - 2 are read
+        const uint32_t d = tmem + kTmemS + 64 * (i & 1);
+        uint32_t ready = 0;  // of the four parts
 #pragma unroll 1
-          for (int u = 0; u < 4; ++u) {
-            if (!wait1(kBarVF + u, i)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint64_t a = dP + (((u >> 1) * kBlk + 32 * (2 * (u & 1) + kk)) >> 4);
-              const uint64_t b = dV + ((2 * u + kk) * 2048 >> 4);
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma_pair(tmem + kTmemO + 128 * j, a, b + (2 * j * kVBlk >> 4), kIdO, !(first && u == 0 && kk == 0));
-            }
-            commit_pair(bar(kBarVE + u));
-          }
-          commit_pair(bar(kBarO));
-          return true;
-        };
-        bool ok = true, pending = false, prev_first = false;
-        int i = 0, n_items = 0;
-        for (; ok; ++i) {
-          if (!(ok = wait1(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)))) break;
-          const int meta = s_meta[i % kPairRing];
-          mbar_arrive(bar(kBarTaken + i % kPairRing));
-          if (meta & kStop) break;
-          const bool first = meta & kFirst;
-          if (first) {
-            // the last row's last product goes before the wait for this row's queries
-            if (pending && !(ok = output(i - 1, prev_first))) break;
-            pending = false;
-            if (!(ok = wait1(kBarQF, n_items++))) break;
-          }
-          const uint32_t d = tmem + kTmemS + 64 * (i & 1);
-#pragma unroll 1
-          for (int s = 0; s < 4; ++s) {
-            if (!(ok = wait1(kBarKF + s, i))) break;
-            tc_fence_after();
+        for (int s = 0; s < 4; ++s) {
+          if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
+          tc_fence_after();
+          if (elect_one()) {
             const uint32_t off = 2 * s * kBlk;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -351,20 +344,61 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
               for (int k = 0; k < 4; ++k) mma_pair(d, dQ + ((8 * kBlk + 32 * k) >> 4), dK + ((8 * kBlk + 32 * k) >> 4), kIdR, 1);
             }
             commit_pair(bar(kBarKE + s));
+            if (s == 3) {
+              commit_pair(bar(kBarS + (i & 1)));
+              if (meta & kLast) commit_pair(bar(kBarQE));
+            }
           }
-          if (!ok) break;
-          commit_pair(bar(kBarS + (i & 1)));
-          if (meta & kLast) commit_pair(bar(kBarQE));
-          if (pending) ok = output(i - 1, prev_first);
-          pending = true;
-          prev_first = first;
+          __syncwarp();
         }
-        if (ok && pending) output(i - 1, prev_first);
-        // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
-        commit_pair(bar(kBarDrain));
-        int unused = 0;
-        wait_bar(bar(kBarDrain), 0, &unused, g.err);
+        if (!ok) break;
       }
+      // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+      if (elect_one()) commit_pair(bar(kBarDrain));
+      __syncwarp();
+      int unused = 0;
+      wait_bar(bar(kBarDrain), 0, &unused, g.err);
+      __syncwarp();
+    } else if (warp == kMmaO && rank == 0) {
+      // ------------------------------------------------- MMAs of the outputs
+      const uint32_t tmem = *s_tmem;
+      constexpr uint32_t kIdO = idesc_att(128, 256, 0, 0, 1);
+      const uint64_t dP = smem_desc_sw128(sP), dV = desc_mn_sw128(sV, kVBlk);
+      bool ok = true;
+      for (int i = 0;; ++i) {
+        if (!listed(i)) break;
+        const int meta = s_meta[i % kPairRing];
+        taken(i);
+        if (meta & kStop) break;
+        // lane by lane: the four parts of V, the weights
+        const uint32_t mine = bar(lane == 4 ? kBarP : kBarVF + (lane & 3));
+        uint32_t ready = 0;
+        if (!wait_any(ready, 4, lane < 5, mine, i & 1, s_abort, g.err)) break;
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+          if (!(ok = wait_any(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint64_t a = dP + (((u >> 1) * kBlk + 32 * (2 * (u & 1) + kk)) >> 4);
+              const uint64_t b = dV + ((2 * u + kk) * 2048 >> 4);
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                mma_pair(tmem + kTmemO + 128 * j, a, b + (2 * j * kVBlk >> 4), kIdO,
+                         !((meta & kFirst) && u == 0 && kk == 0));
+            }
+            commit_pair(bar(kBarVE + u));
+            if (u == 3) commit_pair(bar(kBarO));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (elect_one()) commit_pair(bar(kBarDrain + 1));
+      __syncwarp();
+      int unused = 0;
+      wait_bar(bar(kBarDrain + 1), 0, &unused, g.err);
       __syncwarp();
     }
   } else if (warp >= kQ) {
@@ -382,12 +416,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       load(16 * w);
       if (!(ok = wait(kBarQE, n + 1) && wait(kBarCE, n + 1))) break;
 #pragma unroll 1
-      for (int r0 = 16 * w;; r0 += 4) {
+      for (int r = 0;; ++r) {
+        store_query_row(v[0], p.scale, smem + kOffQ, kBlk, 16 * w + r, s_c, lane, [](int s) { return s; });
+        if (r == 15) break;
+        if ((r & 3) == 3) {
+          load(16 * w + r + 1);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          store_query_row(v[k], p.scale, smem + kOffQ, kBlk, r0 + k, s_c, lane, [](int s) { return s; });
-        if (r0 == 16 * w + 12) break;
-        load(r0 + 4);
+          for (int k = 0; k < 3; ++k) {
+            v[0][k] = v[1][k];
+            v[1][k] = v[2][k];
+            v[2][k] = v[3][k];
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -403,38 +444,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     const uint32_t row = sV + 2 * half * kVBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
     const uint32_t full = in_first(bar(kBarVF + u));
     RawLatent raw;
-    int meta = 0;
-    auto take = [&](RawLatent& r, int& m, int i) {
-      if (!listed(i)) return false;
-      m = s_meta[i % kPairRing];
-      if (key < (m & 0xFFFF))
-        load_latent(r, p.kv + static_cast<int64_t>(s_ring[i % kPairRing * kTile + key]) * kKvEntry, 2 * rank + half);
-      else
-        zero_latent(r);
-      taken(i);
-      return true;
-    };
-    bool ok = take(raw, meta, 0);
-    for (int i = 0; ok && !(meta & kStop); ++i) {
+    for (int i = -1;; ++i) {  // loads of tile i + 1, then tile i to shared memory
+      if (!listed(i + 1)) break;
       RawLatent next;
-      int m = 0;
-      if (!(ok = take(next, m, i + 1)) || !(ok = wait(kBarVE + u, i + 1))) break;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        __half2 lo, hi;
-        scale_pairs(raw, s, lo, hi);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[4];
-          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
-          sts128(row + (s >> 1) * kVBlk + (((4 * (s & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-        }
+      const int m = s_meta[(i + 1) % kPairRing];
+      if (key < (m & 0xFFFF))
+        load_latent(next, p.kv + static_cast<int64_t>(s_ring[(i + 1) % kPairRing * kTile + key]) * kKvEntry, 2 * rank + half);
+      else
+        zero_latent(next);
+      taken(i + 1);
+      if (i >= 0) {
+        if (!wait(kBarVE + u, i + 1)) break;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) decode_step(raw, row + (s >> 1) * kVBlk + ((((4 * s) ^ sw) & 4) << 4), sw & 3);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(full);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(full);
+      if (m & kStop) break;
       raw = next;
-      meta = m;
     }
   } else if (warp >= kK) {
     // ----------------------------------------------------------------- K
@@ -443,54 +471,43 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     const uint32_t full = in_first(bar(kBarKF));
     RawLatent raw;
     uint32_t rope[8];
-    int meta = 0;
-    auto take = [&](RawLatent& r, uint32_t (&ro)[8], int& m, int i) {
-      if (!listed(i)) return false;
-      m = s_meta[i % kPairRing];
-      const int k = rank * kHalf + key;
-      if (k < (m & 0xFFFF)) {
-        const uint8_t* e = p.kv + static_cast<int64_t>(s_ring[i % kPairRing * kTile + k]) * kKvEntry;
-        load_latent(r, e, part);
-        ldg256(ro, e + kKvRopeOff + part * 32);
-      } else {
-        zero_latent(r);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) ro[x] = 0u;
-      }
-      taken(i);
-      return true;
-    };
-    bool ok = take(raw, rope, meta, 0);
-    for (int i = 0; ok && !(meta & kStop); ++i) {
+    bool ok = true;
+    for (int i = -1; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
+      if (!listed(i + 1)) break;
       RawLatent next;
       uint32_t next_rope[8];
-      int m = 0;
-      if (!(ok = take(next, next_rope, m, i + 1))) break;
+      const int m = s_meta[(i + 1) % kPairRing];
+      if (rank * kHalf + key < (m & 0xFFFF)) {
+        const uint8_t* e =
+            p.kv + static_cast<int64_t>(s_ring[(i + 1) % kPairRing * kTile + rank * kHalf + key]) * kKvEntry;
+        load_latent(next, e, part);
+        ldg256(next_rope, e + kKvRopeOff + part * 32);
+      } else {
+        zero_latent(next);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (!(ok = wait(kBarKE + s, i + 1))) break;
-        if (s == 0) {
-          const uint32_t dst = sK + 8 * kBlk + key * 128;
-          sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);
-          sts128(dst + (((2 * part + 1) ^ sw) << 4), rope[4], rope[5], rope[6], rope[7]);
-        }
-        __half2 lo, hi;
-        scale_pairs(raw, s, lo, hi);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[4];
-          decode8(raw.code[4 * s + k], k < 2 ? lo : hi, o);
-          sts128(row + 2 * s * kBlk + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(full + 8 * s);
+        for (int x = 0; x < 8; ++x) next_rope[x] = 0u;
       }
-      if (!ok) break;
+      taken(i + 1);
+      if (i >= 0) {
+        uint32_t ready = 0;  // of the four parts
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort, g.err))) break;
+          if (s == 0) {
+            const uint32_t dst = sK + 8 * kBlk + key * 128;
+            sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);
+            sts128(dst + (((2 * part + 1) ^ sw) << 4), rope[4], rope[5], rope[6], rope[7]);
+          }
+          decode_step(raw, row + 2 * s * kBlk + ((((4 * part) ^ sw) & 4) << 4), sw & 3);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(full + 8 * s);
+        }
+      }
+      if (m & kStop) break;
       raw = next;
 #pragma unroll
       for (int x = 0; x < 8; ++x) rope[x] = next_rope[x];
-      meta = m;
     }
   } else {
     // ----------------------------------------------------------- softmax
@@ -498,7 +515,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     const uint32_t tmem = *s_tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = tid & (kHalf - 1), part = tid >> 6;  // head; half of the keys and of the dimensions
     const int bar_id = 1 + (warp & 1);
-    const uint32_t full = in_first(bar(kBarP));
+    const uint32_t full = in_first(bar(kBarP)), read = in_first(bar(kBarSE));
     const uint32_t p_row = sP + part * kBlk + row * 128, sw = static_cast<uint32_t>(row & 7);
     // a word of this thread's and its partner's rows of P, while P is not in use
     volatile float* mine = reinterpret_cast<volatile float*>(smem + kOffP + part * kBlk + row * 128);
@@ -525,33 +542,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
           if (lane == 0) mbar_arrive(bar(kBarCE));
         }
         tc_fence_after();
-        float x[kHalf];
-        bool moved = false;
-#pragma unroll 1
-        for (int pass = 0;; ++pass) {
-          // x <- score - reference, -inf behind the last key; mx: the largest
-          uint32_t (&u)[kHalf] = reinterpret_cast<uint32_t(&)[kHalf]>(x);
-          tmem_ld32(tmem + kTmemS + 64 * (i & 1), reinterpret_cast<uint32_t(&)[32]>(u[0]));
-          tmem_ld32(tmem + kTmemS + 64 * (i & 1) + 32, reinterpret_cast<uint32_t(&)[32]>(u[32]));
+        const uint32_t ts = tmem + kTmemS + 64 * (i & 1);
+        // 32 scores, relative to the reference, -inf behind the last key
+        float x[32];
+        auto scores = [&](int q) {
+          tmem_ld32(ts + 32 * q, reinterpret_cast<uint32_t(&)[32]>(x));
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < kHalf; k += 2) {
+          for (int k = 0; k < 32; k += 2) {
             const float2 a = __ffma2_rn(make_float2(x[k], x[k + 1]), make_float2(c, c), make_float2(m, m));
             x[k] = a.x;
             x[k + 1] = a.y;
           }
           if (n_keys < kHalf) {
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k)
-              if (k >= n_keys) x[k] = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if (32 * q + k >= n_keys) x[k] = -INFINITY;
           }
-          if (pass > 0) break;
-          float mx = fmaxf(x[0], x[1]);
+        };
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          scores(q);
 #pragma unroll
-          for (int k = 2; k < kHalf; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
-          // the same decision in both warps of these heads; a wait that gave up goes this way too
-          moved = heads_bar_or(bar_id, !ok || first || mx > kRise);
-          if (!moved) break;
+          for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+        }
+        // the same decision in both warps of these heads; a wait that gave up goes this way too
+        if (heads_bar_or(bar_id, !ok || first || mx > kRise)) {
           if (!first) ok = wait(kBarO, i - 1) && ok;
           if (heads_bar_or(bar_id, !ok)) {
             ok = false;
@@ -579,26 +596,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
             }
             tmem_wait_st();
           }
+        } else {
+          // P of the last tile has to be consumed before it is overwritten
+          ok = wait(kBarO, i - 1) && ok;
         }
-        if (moved && !ok) break;  // decided by both warps
         float2 sum = make_float2(0.f, 0.f);
-        uint32_t w[kHalf / 2];
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          scores(q);
+          uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < kHalf; k += 2) {
-          const float2 a = make_float2(ex2(x[k]), ex2(x[k + 1]));
-          sum = __fadd2_rn(sum, a);
-          const __half2 h = __floats2half2_rn(a.x, a.y);
-          w[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int k = 0; k < 32; k += 2) {
+            const float2 a = make_float2(ex2(x[k]), ex2(x[k + 1]));
+            sum = __fadd2_rn(sum, a);
+            const __half2 h = __floats2half2_rn(a.x, a.y);
+            w[k >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(p_row + (((4 * q + k) ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         }
         l += sum.x + sum.y;
-        // P of the last tile is consumed (checked above when the reference moved, at the end of the last row)
-        if (!moved && !first) ok = wait(kBarO, i - 1) && ok;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sts128(p_row + ((k ^ sw) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(full);
+        if (lane == 0) {
+          arrive_cluster(full);
+          arrive_cluster(read + 8 * (i & 1));
+        }
       }
       // ---------------------------------------------------------- output
       ok = ok && wait(kBarO, i - 1);
@@ -720,7 +745,8 @@ cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int s
   const PairPlan P = plan_pair(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PairGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(P.items), reinterpret_cast<float*>(ws + P.off_o),
-             reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws)};
+             reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws),
+             page_div(p.page_size)};
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
