@@ -53,20 +53,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // were not ready.
 __device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
                                          volatile int* abort_flag, uint32_t* err) {
-  uint64_t t0 = 0;
-#pragma unroll 1
-  for (uint32_t n = 1; !((ready >> which) & 1u); ++n) {
+  if (!((ready >> which) & 1u)) {
     ready = __ballot_sync(~0u, has && mbar_test(bar, parity));
-    if (n & 255u) continue;
-    const uint64_t now = globaltimer();
-    if (t0 == 0) t0 = now;
-    bool stop = *abort_flag != 0;
-    if (now - t0 > kWaitTimeoutNs) {
-      *abort_flag = 1;
-      atomicOr(err, kErrTimeout);
-      stop = true;
+    if (!((ready >> which) & 1u)) {
+      // the blocking look: polling would take the shared memory's time
+      const bool ok = wait_bar(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, err);
+      if (!__all_sync(~0u, ok)) return false;
+      ready |= 1u << which;
     }
-    if (__any_sync(~0u, stop)) return false;
   }
   return true;
 }
