@@ -61,8 +61,8 @@ constexpr int kParts = kKvLat / 128;             // hand-over parts of a tile bu
 constexpr uint32_t kBlockBytes = kKt * 128;      // one column block
 constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
 constexpr int kSoftWarps = 4, kLoadWarps = 16;   // loaders: two groups of 8 warps, 8 keys a warp
-constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1;
-constexpr int kAttThreads = (kListWarp + 3) * 32;     // whole warpgroups: two warps of the last one idle
+constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1, kMmaOWarp = kMmaWarp + 2;
+constexpr int kAttThreads = (kMmaWarp + 4) * 32;       // whole warpgroups: one warp of the last one idles
 constexpr int kWorkThreads = (kSoftWarps + kLoadWarps) * 32;
 // registers per thread: 80 at launch, then shared out by warpgroup
 constexpr uint32_t kSoftRegs = 136, kLoadRegs = 72, kIssueRegs = 56;
@@ -81,8 +81,8 @@ struct AttSmem {
   static constexpr uint32_t off_ring = off_f + NH * 4;   // pool rows of the next tiles' keys
   static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // keys of each ring tile, then of each buffer
   static constexpr uint32_t off_bars = off_count + (kRing + 2) * 4;
-  // part full and empty [2 buffers][4], ring full and empty, scores [2], weights, output, drain
-  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 2 + 3;
+  // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], weights, output, drain [2]
+  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 4 + 4;
   static constexpr uint32_t off_misc = off_bars + 8 * n_bars;
   static constexpr uint32_t bytes = off_misc + 16;
   static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
@@ -145,6 +145,13 @@ __device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&v)[4
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
+// Four 8 x 8 matrices of 16-bit fragments: lane 8 i + r gives the address of
+// row r of matrix i.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
 // Bulk copy shared -> global (16-byte aligned, whole 16 bytes) and the wait until this thread's copies have read it.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
@@ -184,21 +191,20 @@ __device__ __forceinline__ constexpr int part_dim(int s) { return 2 * (s & 1) + 
 template <int NH>
 __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
                                               int warp, int n_warps, int lane) {
-  using L = AttSmem<NH>;
-  for (int r0 = warp; r0 < NH; r0 += 2 * n_warps) {
-    uint4 v[2][3];
+  auto live = [&](int r) { return r < NH && h0 + r < p.H; };
+  uint4 v[2][3];
+  load_query_row(v[0], p, t, h0 + warp, live(warp), lane);
+  load_query_row(v[1], p, t, h0 + warp + n_warps, live(warp + n_warps), lane);
+#pragma unroll 1
+  for (int r = warp; r < NH; r += n_warps) {
+    uint4 now[3];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int r = r0 + w * n_warps;
-      const bool live = r < NH && h0 + r < p.H;
-      load_query_row(v[w], p, t, h0 + r, live, lane);
+    for (int k = 0; k < 3; ++k) {
+      now[k] = v[0][k];
+      v[0][k] = v[1][k];
     }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int r = r0 + w * n_warps;
-      if (r >= NH) break;
-      store_query_row(v[w], p.scale, smem, L::q_block, r, s_c, lane, part_dim);
-    }
+    load_query_row(v[1], p, t, h0 + r + 2 * n_warps, live(r + 2 * n_warps), lane);
+    store_query_row(now, p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_dim);
   }
 }
 
@@ -215,7 +221,9 @@ template <int NH>
 __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const AttendParams p, const AttGrid g) {
   using L = AttSmem<NH>;
   constexpr uint32_t kTmemO = 0, kTmemS = kParts * NH;  // columns
-  constexpr uint32_t kTmemCols = (kParts + 2) * NH <= 128 ? 128u : (kParts + 2) * NH <= 256 ? 256u : 512u;
+  // all of the tensor memory, so that it begins at column 0 (a constant for the
+  // MMAs); shared memory keeps a second block off the SM anyway
+  constexpr uint32_t kTmemCols = 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -232,7 +240,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   auto bar_listed = [&](int r) { return bars + 8 * (4 * kParts + r); };
   auto bar_taken = [&](int r) { return bars + 8 * (4 * kParts + kRing + r); };
   auto bar_s = [&](int b) { return bars + 8 * (4 * kParts + 2 * kRing + b); };
-  const uint32_t bar_p = bar_s(2), bar_o = bar_p + 8, bar_drain = bar_p + 16;
+  auto bar_read = [&](int b) { return bar_s(2 + b); };
+  const uint32_t bar_p = bar_s(4), bar_o = bar_p + 8, bar_drain = bar_p + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::off_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::off_misc + 8);
 
@@ -261,7 +270,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     mbar_init(bar_s(1), 1);
     mbar_init(bar_p, kSoftWarps);
     mbar_init(bar_o, 1);
+    mbar_init(bar_read(0), kSoftWarps);
+    mbar_init(bar_read(1), kSoftWarps);
     mbar_init(bar_drain, 1);
+    mbar_init(bar_drain + 8, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(bar_listed(r), 1);
       mbar_init(bar_taken(r), kLoadWarps);
@@ -293,154 +305,168 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       // Packs the pool rows of the entries that name a key into tiles, ahead of
       // the gathering warps; a tile of 0 keys ends the list.
       const int32_t* table = p.block_table + static_cast<int64_t>(seq) * p.max_blocks;
-      int total = 0;  // keys packed; total / kKt tiles are published
+      int tile = 0, keys = 0;  // the open tile, and how many keys it has
       bool ok = true, bad = false;
-      auto open_tile = [&](int tile) {  // before the first write to a ring tile
-        return __all_sync(~0u, wait_bar(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
-      };
-      auto publish = [&](int tile, int count) {
-        if (lane == 0) s_ring_n[tile % kRing] = count;
+      auto publish = [&] {
+        if (lane == 0) s_ring_n[tile % kRing] = keys;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
       };
-      int pos[4];
-      auto fetch = [&](int j0) {
+      auto turn = [&] {  // publishes the open tile and opens the next one
+        publish();
+        ++tile;
+        keys = 0;
+        ok = __all_sync(~0u, wait_bar(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
+      };
+      int j0 = j_lo, pos[4];
+      auto fetch = [&] {
 #pragma unroll
         for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
+        j0 += 128;
       };
-      fetch(j_lo);
-      for (int j0 = j_lo; j0 < j_hi && ok; j0 += 128) {
+      fetch();
+#pragma unroll 1
+      for (int left = (j_hi - j_lo + 127) >> 7; left > 0 && ok; --left) {  // steps of 128 entries
         int slot[4];
         slots_of(p, g.div, table, pos, slot, bad);
-        fetch(j0 + 128);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t m = __ballot_sync(~0u, slot[k] >= 0);
-          const int cnt = __popc(m), at = total + __popc(m & lanemask_lt()), end = total + cnt;
-          if (cnt == 0) continue;
-          // a tile is opened by the batch that writes its first key
-          const int first = (total + kKt - 1) / kKt, last = (end - 1) / kKt;
-          if (last >= first && !(ok = open_tile(last))) break;
-          if (slot[k] >= 0) s_ring[at % (kRing * kKt)] = slot[k];
-          __syncwarp();
-          if (end / kKt > total / kKt) publish(total / kKt, kKt);
-          total = end;
+        fetch();
+#pragma unroll 1
+        for (int k = 0; k < 4 && ok; ++k) {
+          const int mine = slot[0];
+          slot[0] = slot[1];
+          slot[1] = slot[2];
+          slot[2] = slot[3];
+          const uint32_t m = __ballot_sync(~0u, mine >= 0);
+          const int at = keys + __popc(m & lanemask_lt());
+          if (mine >= 0 && at < kKt) s_ring[tile % kRing * kKt + at] = mine;
+          keys += __popc(m);
+          if (keys >= kKt) {
+            const int rest = keys - kKt;
+            keys = kKt;
+            turn();
+            if (mine >= 0 && at >= kKt) s_ring[tile % kRing * kKt + at - kKt] = mine;
+            keys = rest;
+          }
         }
       }
-      if (ok && total % kKt) {
-        publish(total / kKt, total % kKt);
-        total += kKt - total % kKt;
-      }
-      if (ok && open_tile(total / kKt)) publish(total / kKt, 0);
+      if (ok && keys > 0) turn();
+      if (ok) publish();
       if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
     } else if (warp == kMmaWarp) {
-      // ---------------------------------------------------------------- MMA
-      const uint32_t tmem = *s_tmem;
-      if (elect_one()) {
-        constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0, 0), kIdR = idesc_att(64, NH, 1, 0, 0), kIdO = idesc_att(128, NH, 0, 1, 1);
-        // descriptors advance by their 16-byte address field
-        const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ), dV = desc_mn_sw128(sK, kBlockBytes),
-                       dP = desc_mn_sw128(sP, kBlockBytes);
-        bool ok = true;
-        auto output = [&](int i) {  // O^T += V^T P^T of tile i
-          const int b = i & 1;
-          if (!wait_bar(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err)) return false;
-          tc_fence_after();
-#pragma unroll 1  // 4 x 4 MMAs: unrolled, their descriptors spill
-          for (int s = 0; s < kParts; ++s) {
-            const uint64_t v = dV + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4);
-#pragma unroll
-            for (int k = 0; k < kKt / 16; ++k)
-              mma_bf16(tmem + kTmemO + s * NH, v + (k * 2048 >> 4), dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
-            mma_commit(bar_empty(b, s));
-          }
-          mma_commit(bar_o);
-          return true;
-        };
-        int i = 0;
-        for (; ok; ++i) {
-          const int b = i & 1;
-          const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
-          if (!(ok = wait_bar(bar_full(b, 0), ph, s_abort, g.err)) || s_n[b] == 0) break;
+      // -------------------------------------------------- MMAs of the scores
+      constexpr uint32_t tmem = 0;
+      constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0, 0), kIdR = idesc_att(64, NH, 1, 0, 0);
+      const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ);
+      const uint32_t leader = elect_one();
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int b = i & 1;
+        const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
+        // lane by lane: the tile's four parts, and that the scores of tile i - 2 are read
+        const uint32_t mine = lane == 4 ? bar_read(b) : bar_full(b, lane & 3), par = lane == 4 ? ph ^ 1u : ph;
+        uint32_t ready = 0;
+        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, g.err)) || s_n[b] == 0) break;
+        if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort, g.err))) break;
 #pragma unroll 1
-          for (int s = 0; s < kParts; ++s) {
-            if (s > 0 && !(ok = wait_bar(bar_full(b, s), ph, s_abort, g.err))) break;
-            tc_fence_after();
-            const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
+        for (int s = 0; s < kParts; ++s) {
+          if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, g.err))) break;
+          tc_fence_after();
+          const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_bf16(d, k0 + (((k >> 2) * kBlockBytes + 32 * (k & 3)) >> 4),
-                       q0 + (((k >> 2) * L::q_block + 32 * (k & 3)) >> 4), kIdS, s > 0 || k > 0);
-            if (s == 1) {  // each group brings half of the rotary block with its first part
+          for (int k = 0; k < 8; ++k)
+            mma_if<1>(leader, d, k0 + (((k >> 2) * kBlockBytes + 32 * (k & 3)) >> 4),
+                      q0 + (((k >> 2) * L::q_block + 32 * (k & 3)) >> 4), kIdS, s > 0 || k > 0);
+          if (s == 1) {  // each group brings half of the rotary block with its first part
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_bf16(d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4), dQ + ((8 * L::q_block + 32 * k) >> 4),
-                         kIdR, 1);
-            }
+            for (int k = 0; k < 4; ++k)
+              mma_if<1>(leader, d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4),
+                        dQ + ((8 * L::q_block + 32 * k) >> 4), kIdR, 1);
           }
-          if (!ok) break;
-          mma_commit(bar_s(b));
-          if (i > 0) ok = output(i - 1);
+          if (s == kParts - 1) commit_if(leader, bar_s(b));
         }
-        if (ok && i > 0) output(i - 1);
-        // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
-        mma_commit(bar_drain);
-        int unused = 0;
-        wait_bar(bar_drain, 0, &unused, g.err);
       }
+      // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+      commit_if(leader, bar_drain);
+      int unused = 0;
+      wait_bar(bar_drain, 0, &unused, g.err);
+      __syncwarp();
+    } else if (warp == kMmaOWarp) {
+      // ------------------------------------------------- MMAs of the outputs
+      constexpr uint32_t tmem = 0;
+      constexpr uint32_t kIdO = idesc_att(128, NH, 0, 1, 1);
+      const uint64_t dV = desc_mn_sw128(sK, kBlockBytes), dP = desc_mn_sw128(sP, kBlockBytes);
+      const uint32_t leader = elect_one();
+      for (int i = 0;; ++i) {  // O^T += V^T P^T of tile i
+        const int b = i & 1;
+        if (!__all_sync(~0u, wait_bar(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) || s_n[b] == 0) break;
+        if (!__all_sync(~0u, wait_bar(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err))) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int s = 0; s < kParts; ++s) {
+          const uint64_t v = dV + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < kKt / 16; ++k)
+            mma_if<1>(leader, tmem + kTmemO + s * NH, v + (k * 2048 >> 4), dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
+          commit_if(leader, bar_empty(b, s));
+        }
+        commit_if(leader, bar_o);
+      }
+      commit_if(leader, bar_drain + 8);
+      int unused = 0;
+      wait_bar(bar_drain + 8, 0, &unused, g.err);
       __syncwarp();
     }
   } else if (warp >= kSoftWarps) {
     regs_dec<kLoadRegs>();
-    const uint32_t tmem = *s_tmem;
+    constexpr uint32_t tmem = 0;
     // ------------------------------------------------------------- gather
     const int lw = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3;
     const int key = lw * 8 + (lane & 7), part = lane >> 3;
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
     RawKey raw;
-    int n_keys = 0;
-    auto take = [&](RawKey& r, int& count, int tile) {  // a tile's loads, once its slots are listed
-      const int k = tile % kRing;
-      if (!__all_sync(~0u, wait_bar(bar_listed(k), static_cast<uint32_t>(tile / kRing) & 1u, s_abort, g.err))) return false;
-      count = s_ring_n[k];
-      load_raw(r, p.kv, s_ring[k * kKt + key], key < count, part, group);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_taken(k));
-      return true;
-    };
-    bool ok = take(raw, n_keys, 0);
-    int i = 0;
-    for (; ok; ++i) {
-      const int b = i & 1;
-      const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
+    int n_keys = 0, i = -1;
+    for (bool ok = true; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
       RawKey next;
       int n_next = 0;
-      if (n_keys > 0 && !(ok = take(next, n_next, i + 1))) break;
-      const uint32_t tile = sK + b * kTileBytes + row;
-#pragma unroll
-      for (int u = 0; u < kParts / 2; ++u) {
-        const int s = 2 * u + group;
-        if (!(ok = __all_sync(~0u, wait_bar(bar_empty(b, s), ph, s_abort, g.err)))) break;
-        if (u == 0) {
-          if (warp == kSoftWarps && lane == 0) s_n[b] = n_keys;
-          sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
-        }
-        const __half2 sc = __half2(
-            __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>((raw.scale >> (16 * u)) & 0xFFFFu), __NV_E4M3));
-        const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
-        const uint32_t dst = tile + (2 * s + (part >> 1)) * kBlockBytes;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[4];
-          decode8(raw.code[4 * u + k], k < 2 ? lo : hi, o);
-          sts128(dst + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
-        }
-        fence_proxy_async_smem();
+      if (i < 0 || n_keys > 0) {
+        const int k = (i + 1) % kRing;
+        if (!__all_sync(~0u, wait_bar(bar_listed(k), static_cast<uint32_t>((i + 1) / kRing) & 1u, s_abort, g.err))) break;
+        n_next = s_ring_n[k];
+        load_raw(next, p.kv, s_ring[k * kKt + key], key < n_next, part, group);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_full(b, s));
-        if (n_keys == 0) break;  // the end of the list: part 0 alone carries it
+        if (lane == 0) mbar_arrive(bar_taken(k));
       }
-      if (!ok || n_keys == 0) break;
+      if (i >= 0) {
+        const int b = i & 1;
+        const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
+        const uint32_t tile = sK + b * kTileBytes + row;
+#pragma unroll 1
+        for (int u = 0; u < kParts / 2; ++u) {
+          const int s = 2 * u + group;
+          if (!(ok = __all_sync(~0u, wait_bar(bar_empty(b, s), ph, s_abort, g.err)))) break;
+          if (u == 0) {
+            if (warp == kSoftWarps && lane == 0) s_n[b] = n_keys;
+            sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
+          }
+          const __half2 sc =
+              __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(raw.scale & 0xFFFFu), __NV_E4M3));
+          const __half2 lo = __low2half2(sc), hi = __high2half2(sc);
+          const uint32_t dst = tile + (2 * s + (part >> 1)) * kBlockBytes;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[4];
+            decode8(raw.code[k], k < 2 ? lo : hi, o);
+            sts128(dst + (((4 * (part & 1) + k) ^ sw) << 4), o[0], o[1], o[2], o[3]);
+            raw.code[k] = raw.code[k + 4];
+          }
+          raw.scale >>= 16;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_full(b, s));
+          if (n_keys == 0) break;  // the end of the list: part 0 alone carries it
+        }
+        if (n_keys == 0) break;
+      }
       raw = next;
       n_keys = n_next;
     }
@@ -495,101 +521,90 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     }
   } else {
     regs_inc<kSoftRegs>();
-    const uint32_t tmem = *s_tmem;
+    constexpr uint32_t tmem = 0;
     // ------------------------------------------------------------ softmax
     // Threads hold pairs of columns (heads): pair j is columns 8 j + 2 (lane %
     // 4) and the next, at keys (rows) r0 and r0 + 8 of the warp's 16.
     constexpr int C = NH / 8;
-    float2 c[C], m[C], l[C];  // factor to log2 units, negated reference, sum
+    float2 c[C], m[C], l[C];  // factor to log2 units, negated reference (from the first tile on), sum
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       c[j] = *reinterpret_cast<const float2*>(s_c + 8 * j + 2 * (lane & 3));
-      m[j] = make_float2(INFINITY, INFINITY);
+      m[j] = make_float2(0.f, 0.f);
       l[j] = make_float2(0.f, 0.f);
     }
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const int r0 = lane >> 2;
-    const uint32_t p0 = sP + (warp * 16 + r0) * 128 + (lane & 3) * 4;
+    const uint32_t p0 = sP + (warp * 16 + (lane & 15)) * 128;  // this lane's row in the 8 x 8 stores
     float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH], while P is not in use
     bool ok = true;
-    int nt = 0;  // tiles
-    for (int i = 0;; nt = ++i) {
+    for (int i = 0;; ++i) {
       const int b = i & 1;
       ok = __all_sync(~0u, wait_bar(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const int n_keys = ok ? s_n[b] : 0;
       if (n_keys > 0)
         ok = __all_sync(~0u, wait_bar(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
       const bool end = !ok || n_keys == 0;
-      bool rise = end;
       float x[NH / 2];
-      auto scores = [&] {  // x <- score - reference, -inf behind the last key; the largest
-        uint32_t u[NH / 2];
-        tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, u);
-        tmem_wait_ld();
+      bool moved = false;
+      tc_fence_after();
+#pragma unroll 1
+      for (int pass = 0;; ++pass) {
         float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const float2 a = __ffma2_rn(make_float2(__uint_as_float(u[4 * j]), __uint_as_float(u[4 * j + 1])), c[j], m[j]);
-          const float2 d = __ffma2_rn(make_float2(__uint_as_float(u[4 * j + 2]), __uint_as_float(u[4 * j + 3])), c[j], m[j]);
-          x[4 * j] = a.x;
-          x[4 * j + 1] = a.y;
-          x[4 * j + 2] = d.x;
-          x[4 * j + 3] = d.y;
-        }
-        if (n_keys < kKt) {
-          const bool v0 = warp * 16 + r0 < n_keys, v1 = warp * 16 + 8 + r0 < n_keys;
-#pragma unroll
-          for (int k = 0; k < NH / 2; ++k)
-            if (!(k & 2 ? v1 : v0)) x[k] = -INFINITY;
-        }
-#pragma unroll
-        for (int k = 0; k < NH / 2; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
-        return mx;
-      };
-      if (!end) {
-        tc_fence_after();
-        rise = scores() > kRise;
-      }
-      // the same decision in all four warps; the end of the list and a wait that gave up go this way too
-      const bool moved = soft_bar_or(rise);
-      if (moved) {
-        if (i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
-        if (soft_bar_or(end || !ok)) break;
-        tc_fence_after();
-        {
-          uint32_t u[NH / 2];
-          tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, u);
+        if (!end) {  // x <- score - reference, -inf behind the last key; mx: the largest
+          tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, reinterpret_cast<uint32_t(&)[NH / 2]>(x));
           tmem_wait_ld();
-          const bool v0 = warp * 16 + r0 < n_keys, v1 = warp * 16 + 8 + r0 < n_keys;
 #pragma unroll
           for (int j = 0; j < C; ++j) {
-            float2 mx = make_float2(-INFINITY, -INFINITY);
-            if (v0) mx = make_float2(__uint_as_float(u[4 * j]) * c[j].x, __uint_as_float(u[4 * j + 1]) * c[j].y);
-            if (v1) {
-              mx.x = fmaxf(mx.x, __uint_as_float(u[4 * j + 2]) * c[j].x);
-              mx.y = fmaxf(mx.y, __uint_as_float(u[4 * j + 3]) * c[j].y);
-            }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              mx.x = fmaxf(mx.x, __shfl_xor_sync(~0u, mx.x, o));
-              mx.y = fmaxf(mx.y, __shfl_xor_sync(~0u, mx.y, o));
-            }
-            if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = mx;
+            const float2 a = __ffma2_rn(make_float2(x[4 * j], x[4 * j + 1]), c[j], m[j]);
+            const float2 d = __ffma2_rn(make_float2(x[4 * j + 2], x[4 * j + 3]), c[j], m[j]);
+            x[4 * j] = a.x;
+            x[4 * j + 1] = a.y;
+            x[4 * j + 2] = d.x;
+            x[4 * j + 3] = d.y;
           }
+          if (n_keys < kKt) {
+            const bool v0 = warp * 16 + r0 < n_keys, v1 = warp * 16 + 8 + r0 < n_keys;
+#pragma unroll
+            for (int k = 0; k < NH / 2; ++k)
+              if (!(k & 2 ? v1 : v0)) x[k] = -INFINITY;
+          }
+#pragma unroll
+          for (int k = 0; k < NH / 2; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+        }
+        if (pass > 0) break;
+        // the same decision in all four warps; the first tile, the end of the
+        // list and a wait that gave up go this way too
+        moved = soft_bar_or(end || i == 0 || mx > kRise);
+        if (!moved) break;
+        if (i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+        if (soft_bar_or(end || !ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          float2 t = make_float2(fmaxf(x[4 * j], x[4 * j + 2]) - m[j].x, fmaxf(x[4 * j + 1], x[4 * j + 3]) - m[j].y);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            t.x = fmaxf(t.x, __shfl_xor_sync(~0u, t.x, o));
+            t.y = fmaxf(t.y, __shfl_xor_sync(~0u, t.y, o));
+          }
+          if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = t;
         }
         named_bar_sync(1, kSoftThreads);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
           const int col = 8 * j + 2 * (lane & 3);
-          float2 n = make_float2(-m[j].x, -m[j].y), f = make_float2(1.f, 1.f);
+          float2 n = i > 0 ? make_float2(-m[j].x, -m[j].y) : make_float2(-INFINITY, -INFINITY);
 #pragma unroll
           for (int w = 0; w < kSoftWarps; ++w) {
             const float2 e = *reinterpret_cast<const float2*>(exch + w * NH + col);
             n.x = fmaxf(n.x, e.x);
             n.y = fmaxf(n.y, e.y);
           }
-          if (n.x != -INFINITY) f.x = ex2(-m[j].x - n.x);
-          if (n.y != -INFINITY) f.y = ex2(-m[j].y - n.y);
+          const float2 f = i > 0 ? make_float2(ex2(-m[j].x - n.x), ex2(-m[j].y - n.y)) : make_float2(1.f, 1.f);
           m[j] = make_float2(-n.x, -n.y);
           l[j].x *= f.x;
           l[j].y *= f.y;
@@ -608,8 +623,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           }
           tmem_wait_st();
         }
-        scores();
       }
+      if (moved && !ok) break;  // decided by all four warps
       uint32_t w[NH / 4];
 #pragma unroll
       for (int j = 0; j < C; ++j) {
@@ -620,16 +635,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hd);
       }
       // P of the last tile is consumed (checked above when the reference moved)
-      if (!moved && i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
+      if (!moved) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        sts32(p0 + ((j ^ r0) << 4), w[2 * j]);
-        sts32(p0 + ((j ^ r0) << 4) + 8 * 128, w[2 * j + 1]);
-      }
+      for (int j = 0; j < C; j += 2)
+        stmatrix4(p0 + (((j + (lane >> 4)) ^ (lane & 7)) << 4), w[2 * j], w[2 * j + 1], w[2 * j + 2], w[2 * j + 3]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p);
+      if (lane == 0) {
+        mbar_arrive(bar_p);
+        mbar_arrive(bar_read(b));
+      }
     }
     // --------------------------------------------------------- statistics
     // (the loop ended behind the last product: P is not in use)
@@ -653,7 +669,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           const float ref = k ? -m[j].y : -m[j].x;
           const float sum = (exch[col] + exch[NH + col]) + (exch[2 * NH + col] + exch[3 * NH + col]);
           if (g.splits > 1) {
-            g.part_ml[item * NH + col] = make_float2(ref, sum);
+            g.part_ml[item * NH + col] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
           } else {
             s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
             if (p.lse && h0 + col < p.H)

@@ -121,22 +121,6 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Arrive on this barrier of both blocks once the MMAs issued so far complete.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(bar)
-      : "memory");
-}
 // Barrier over the two softmax warps of the same heads, with a predicate.
 __device__ __forceinline__ bool heads_bar_or(int id, bool v) {
   uint32_t r;
@@ -314,9 +298,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       if (__any_sync(~0u, bad) && rank == 0 && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
     } else if (warp == kMma && rank == 0) {
       // -------------------------------------------------- MMAs of the scores
-      const uint32_t tmem = *s_tmem;
+      constexpr uint32_t tmem = 0;  // all 512 columns are allocated
       constexpr uint32_t kIdS = idesc_att(128, 128, 0, 0, 0), kIdR = idesc_att(128, 128, 1, 0, 0);
       const uint64_t dQ = smem_desc_sw128(sQ), dK = smem_desc_sw128(sK);
+      const uint32_t leader = elect_one();
       bool ok = true;
       int n_items = 0;
       for (int i = 0;; ++i) {
@@ -332,38 +317,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         for (int s = 0; s < 4; ++s) {
           if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t off = 2 * s * kBlk;
+          const uint64_t q0 = dQ + (2 * s * kBlk >> 4), k0 = dK + (2 * s * kBlk >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t o = (off + (k >> 2) * kBlk + 32 * (k & 3)) >> 4;
-              mma_pair(d, dQ + o, dK + o, kIdS, s > 0 || k > 0);
-            }
-            if (s == 0) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_pair(d, dQ + ((8 * kBlk + 32 * k) >> 4), dK + ((8 * kBlk + 32 * k) >> 4), kIdR, 1);
-            }
-            commit_pair(bar(kBarKE + s));
-            if (s == 3) {
-              commit_pair(bar(kBarS + (i & 1)));
-              if (meta & kLast) commit_pair(bar(kBarQE));
-            }
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t o = ((k >> 2) * kBlk + 32 * (k & 3)) >> 4;
+            mma_if<2>(leader, d, q0 + o, k0 + o, kIdS, s > 0 || k > 0);
           }
-          __syncwarp();
+          if (s == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_if<2>(leader, d, dQ + ((8 * kBlk + 32 * k) >> 4), dK + ((8 * kBlk + 32 * k) >> 4), kIdR, 1);
+          }
+          commit_pair_if(leader, bar(kBarKE + s));
+          if (s == 3) {
+            commit_pair_if(leader, bar(kBarS + (i & 1)));
+            if (meta & kLast) commit_pair_if(leader, bar(kBarQE));
+          }
         }
         if (!ok) break;
       }
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
-      if (elect_one()) commit_pair(bar(kBarDrain));
-      __syncwarp();
+      commit_pair_if(leader, bar(kBarDrain));
       int unused = 0;
       wait_bar(bar(kBarDrain), 0, &unused, g.err);
       __syncwarp();
     } else if (warp == kMmaO && rank == 0) {
       // ------------------------------------------------- MMAs of the outputs
-      const uint32_t tmem = *s_tmem;
+      constexpr uint32_t tmem = 0;  // all 512 columns are allocated
       constexpr uint32_t kIdO = idesc_att(128, 256, 0, 0, 1);
       const uint64_t dP = smem_desc_sw128(sP), dV = desc_mn_sw128(sV, kVBlk);
+      const uint32_t leader = elect_one();
       bool ok = true;
       for (int i = 0;; ++i) {
         if (!listed(i)) break;
@@ -378,25 +361,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         for (int u = 0; u < 4; ++u) {
           if (!(ok = wait_any(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
           tc_fence_after();
-          if (elect_one()) {
+          const uint64_t a0 = dP + (((u >> 1) * kBlk + 64 * (u & 1)) >> 4), b0 = dV + (2 * u * 2048 >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const uint64_t a = dP + (((u >> 1) * kBlk + 32 * (2 * (u & 1) + kk)) >> 4);
-              const uint64_t b = dV + ((2 * u + kk) * 2048 >> 4);
+          for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                mma_pair(tmem + kTmemO + 128 * j, a, b + (2 * j * kVBlk >> 4), kIdO,
-                         !((meta & kFirst) && u == 0 && kk == 0));
-            }
-            commit_pair(bar(kBarVE + u));
-            if (u == 3) commit_pair(bar(kBarO));
+            for (int j = 0; j < 2; ++j)
+              mma_if<2>(leader, tmem + kTmemO + 128 * j, a0 + 2 * kk, b0 + ((kk * 2048 + 2 * j * kVBlk) >> 4), kIdO,
+                        !((meta & kFirst) && u == 0 && kk == 0));
           }
-          __syncwarp();
+          commit_pair_if(leader, bar(kBarVE + u));
+          if (u == 3) commit_pair_if(leader, bar(kBarO));
         }
         if (!ok) break;
       }
-      if (elect_one()) commit_pair(bar(kBarDrain + 1));
-      __syncwarp();
+      commit_pair_if(leader, bar(kBarDrain + 1));
       int unused = 0;
       wait_bar(bar(kBarDrain + 1), 0, &unused, g.err);
       __syncwarp();
@@ -512,7 +490,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   } else {
     // ----------------------------------------------------------- softmax
     regs_inc<kSoftRegs>();
-    const uint32_t tmem = *s_tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t tmem = static_cast<uint32_t>(warp * 32) << 16;
     const int row = tid & (kHalf - 1), part = tid >> 6;  // head; half of the keys and of the dimensions
     const int bar_id = 1 + (warp & 1);
     const uint32_t full = in_first(bar(kBarP)), read = in_first(bar(kBarSE));
@@ -641,7 +619,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       const float f = g.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       if (part == 0 && h < p.H) {
         if (g.splits > 1)
-          g.part_ml[part_row] = make_float2(-m, l);
+          g.part_ml[part_row] = make_float2(l == 0.f ? -INFINITY : -m, l);
         else if (p.lse)
           p.lse[it.t * p.H + h] = l == 0.f ? -INFINITY : (log2f(l) - m) * kLn2;
       }
