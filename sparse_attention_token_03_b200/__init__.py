@@ -559,17 +559,37 @@ def _opt(t, name: str, dtype, shape: tuple, device) -> int | None:
     """Pointer of an optional contiguous tensor of exactly this shape."""
     if t is None:
         return None
-    _need(t, name, dtype, len(shape), device)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    return _arg(t, name, dtype, shape, device)
+
+
+def _arg(t, name: str, dtype, shape: tuple, device) -> int:
+    """Pointer of a contiguous tensor of exactly this shape.  A decode step's
+    calls are as short on the GPU as on the host, so the checks that pass are
+    kept to one expression."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous() and t.is_cuda):
+        _need(t, name, dtype, len(shape), device)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
 def _out(t, name: str, dtype, shape: tuple, device) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _opt(t, name, dtype, shape, device)
+    _arg(t, name, dtype, shape, device)
     return t
+
+
+def _call(entry, device, *args):
+    """Calls a C entry point with `args` and the device's current stream."""
+    if torch.cuda.current_device() == device.index:
+        rc = entry(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = entry(*args, _stream_ptr(device))
+    if rc != DSA_OK:
+        _check(rc)
 
 
 def dsa_block_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor,
@@ -590,51 +610,50 @@ def dsa_block_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_tabl
     _need(cached_len, "cached_len", torch.int32, 1, dev)
     B = cached_len.shape[0]
     _need(block_table, "block_table", torch.int32, 2, dev)
-    _need(free_pages, "free_pages", torch.int32, 1, dev)
-    _opt(new_len, "new_len", torch.int32, (B,), dev)
-    _opt(free_begin, "free_begin", torch.int32, (1,), dev)
-    if new_len is None or free_begin is None or block_table.shape[0] != B:
-        raise ValueError("need new_len (B,), free_begin (1,) and block_table (B, max_blocks)")
+    max_blocks = block_table.shape[1]
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must be ({B}, max_blocks), got {tuple(block_table.shape)}")
     T_cap = int(T_cap)
     if T_cap < 0:
         raise ValueError("T_cap must not be negative")
-    slot_map = _out(slot_map, "slot_map", torch.int32, (T_cap,), dev)
-    position = _out(position, "position", torch.int32, (T_cap,), dev)
-    row_seq = _out(row_seq, "row_seq", torch.int32, (T_cap,), dev)
-    row_start = _out(row_start, "row_start", torch.int32, (B + 1,), dev)
-    seq_len = _out(seq_len, "seq_len", torch.int32, (B,), dev)
-    free_end = _out(free_end, "free_end", torch.int32, (1,), dev)
-    st = _opt(status, "status", torch.int32, (1,), dev)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_block_tables(cached_len.data_ptr(), new_len.data_ptr(), B, block_table.data_ptr(),
-                                      block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
-                                      free_begin.data_ptr(), int(n_pages), int(page_size), T_cap,
-                                      slot_map.data_ptr(), position.data_ptr(), row_seq.data_ptr(),
-                                      row_start.data_ptr(), seq_len.data_ptr(), free_end.data_ptr(), st,
-                                      _stream_ptr(dev)))
+    new = _arg(new_len, "new_len", torch.int32, (B,), dev)
+    begin = _arg(free_begin, "free_begin", torch.int32, (1,), dev)
+    _need(free_pages, "free_pages", torch.int32, 1, dev)
+    if slot_map is None and position is None and row_seq is None and row_start is None and seq_len is None \
+            and free_end is None:
+        # one allocation for the six
+        slot_map, position, row_seq, row_start, seq_len, free_end = block_table.new_empty(
+            3 * T_cap + 2 * B + 2).split_with_sizes([T_cap, T_cap, T_cap, B + 1, B, 1])
+    else:
+        slot_map = _out(slot_map, "slot_map", torch.int32, (T_cap,), dev)
+        position = _out(position, "position", torch.int32, (T_cap,), dev)
+        row_seq = _out(row_seq, "row_seq", torch.int32, (T_cap,), dev)
+        row_start = _out(row_start, "row_start", torch.int32, (B + 1,), dev)
+        seq_len = _out(seq_len, "seq_len", torch.int32, (B,), dev)
+        free_end = _out(free_end, "free_end", torch.int32, (1,), dev)
+    _call(lib().dsa_block_tables, dev, cached_len.data_ptr(), new, B, block_table.data_ptr(), max_blocks, free_pages.data_ptr(),
+          free_pages.shape[0], begin, int(n_pages), int(page_size), T_cap, slot_map.data_ptr(), position.data_ptr(),
+          row_seq.data_ptr(), row_start.data_ptr(), seq_len.data_ptr(), free_end.data_ptr(),
+          _opt(status, "status", torch.int32, (1,), dev))
     return slot_map, position, row_seq, row_start, seq_len, free_end
 
 
 def _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight, q_bias, k_norm, k_weight, k_bias, status):
+    _need(q, "q", torch.bfloat16, 3, None)
     dev = q.device
-    _need(q, "q", torch.bfloat16, 3, dev)
     T, H, d = q.shape
-    _need(k, "k", torch.bfloat16, 2, dev)
-    if tuple(k.shape) != (T, d):
-        raise ValueError("shape mismatch between q (T,H,d) and k (T,d)")
-    _need(position, "position", torch.int32, 1, dev)
+    kp = _arg(k, "k", torch.bfloat16, (T, d), dev)
+    pos = _arg(position, "position", torch.int32, (T,), dev)
     _need(inv_freq, "inv_freq", torch.float32, 1, dev)
-    if position.shape[0] != T:
-        raise ValueError(f"position must be ({T},)")
-    if k_out.dim() < 2 or k_out.shape[-1] != d:
+    if not isinstance(k_out, torch.Tensor) or k_out.dim() < 2 or k_out.shape[-1] != d:
         raise ValueError(f"k_out must hold rows of {d}: (n_slots, {d}) or (n_pages, page_size, {d})")
-    for name in (q_norm, k_norm):
-        if name not in NORMS:
-            raise ValueError(f"norm must be one of {sorted(NORMS)}, got {name!r}")
-    w = [_opt(t, n, torch.float32, (d,), dev) for t, n in
-         ((q_weight, "q_weight"), (q_bias, "q_bias"), (k_weight, "k_weight"), (k_bias, "k_bias"))]
-    head = (q.data_ptr(), k.data_ptr(), position.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], T, H, d,
-            NORMS[q_norm], w[0], w[1], NORMS[k_norm], w[2], w[3])
+    if q_norm not in NORMS or k_norm not in NORMS:
+        raise ValueError(f"norm must be one of {sorted(NORMS)}, got {q_norm!r} and {k_norm!r}")
+    head = (q.data_ptr(), kp, pos, inv_freq.data_ptr(), 2 * inv_freq.shape[0], T, H, d,
+            NORMS[q_norm], _opt(q_weight, "q_weight", torch.float32, (d,), dev),
+            _opt(q_bias, "q_bias", torch.float32, (d,), dev),
+            NORMS[k_norm], _opt(k_weight, "k_weight", torch.float32, (d,), dev),
+            _opt(k_bias, "k_bias", torch.float32, (d,), dev))
     slots = (_opt(slot_map, "slot_map", torch.int32, (T,), dev), k_out.numel() // d)
     return dev, T, H, d, head, slots, _opt(status, "status", torch.int32, (1,), dev)
 
@@ -655,11 +674,9 @@ def dsa_index_prepare(q: torch.Tensor, k: torch.Tensor, position: torch.Tensor, 
     """
     dev, T, H, d, head, slots, st = _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight,
                                                   q_bias, k_norm, k_weight, k_bias, status)
-    _need(k_out, "k_out", torch.bfloat16, k_out.dim(), dev)
+    kp = _arg(k_out, "k_out", torch.bfloat16, k_out.shape, dev)
     q_out = _out(q_out, "q_out", torch.bfloat16, (T, H, d), dev)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_index_prepare(*head, float(eps), int(bool(interleaved)), *slots, q_out.data_ptr(),
-                                       k_out.data_ptr(), st, _stream_ptr(dev)))
+    _call(lib().dsa_index_prepare, dev, *head, float(eps), int(bool(interleaved)), *slots, q_out.data_ptr(), kp, st)
     return q_out, k_out
 
 
@@ -680,14 +697,13 @@ def dsa_index_prepare_fp8(q: torch.Tensor, k: torch.Tensor, position: torch.Tens
     if tuple(qc.shape) != (T, H, d):
         raise ValueError(f"q_out must be {(T, H, d)}")
     q_scale_out = _out(q_scale_out, "q_scale_out", torch.float32, (T, H), dev)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_index_prepare_fp8(*head, float(eps), int(bool(interleaved)), *slots, qc.data_ptr(),
-                                           q_scale_out.data_ptr(), kc.data_ptr(), ks, st, _stream_ptr(dev)))
+    _call(lib().dsa_index_prepare_fp8, dev, *head, float(eps), int(bool(interleaved)), *slots, qc.data_ptr(),
+          q_scale_out.data_ptr(), kc.data_ptr(), ks, st)
     return q_out, q_scale_out, k_out, k_scale_out
 
 
-def _kv4_pool(kv_pages, dev):
-    _need(kv_pages, "kv_pages", torch.uint8, 3, dev)
+def _kv4_pool(kv_pages):
+    _need(kv_pages, "kv_pages", torch.uint8, 3, None)
     if kv_pages.shape[2] != KV4_ENTRY_BYTES:
         raise ValueError(f"kv_pages must be (n_pages, page_size, {KV4_ENTRY_BYTES}), got {tuple(kv_pages.shape)}")
     return kv_pages.shape[0] * kv_pages.shape[1]
@@ -701,20 +717,13 @@ def dsa_kv4_write(latent: torch.Tensor, rope: torch.Tensor, kv_pages: torch.Tens
     (int32; < 0: padding) of the page pool kv_pages (n_pages, page_size, 416)
     uint8.  Returns kv_pages.
     """
+    n_slots = _kv4_pool(kv_pages)
     dev = kv_pages.device
-    n_slots = _kv4_pool(kv_pages, dev)
-    _need(latent, "latent", torch.bfloat16, 2, dev)
-    T = latent.shape[0]
-    if latent.shape[1] != KV4_LATENT:
-        raise ValueError(f"latent must be (T, {KV4_LATENT})")
-    _need(rope, "rope", torch.bfloat16, 2, dev)
     _need(slot_map, "slot_map", torch.int32, 1, dev)
-    if tuple(rope.shape) != (T, KV4_ROPE) or slot_map.shape[0] != T:
-        raise ValueError(f"rope must be ({T}, {KV4_ROPE}) and slot_map ({T},)")
-    st = _opt(status, "status", torch.int32, (1,), dev)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_kv4_write(latent.data_ptr(), rope.data_ptr(), kv_pages.data_ptr(), n_slots,
-                                   slot_map.data_ptr(), T, st, _stream_ptr(dev)))
+    T = slot_map.shape[0]
+    _call(lib().dsa_kv4_write, dev, _arg(latent, "latent", torch.bfloat16, (T, KV4_LATENT), dev),
+          _arg(rope, "rope", torch.bfloat16, (T, KV4_ROPE), dev), kv_pages.data_ptr(), n_slots, slot_map.data_ptr(), T,
+          _opt(status, "status", torch.int32, (1,), dev))
     return kv_pages
 
 
@@ -722,16 +731,14 @@ def dsa_kv4_read(kv_pages: torch.Tensor, slot_map: torch.Tensor, latent_out=None
     """Rows slot_map (T,) int32 of the 4-bit latent cache in bf16 (exact):
     (latent (T, 512), rope (T, 64)).  Rows with a slot < 0 are left as they
     were."""
+    n_slots = _kv4_pool(kv_pages)
     dev = kv_pages.device
-    n_slots = _kv4_pool(kv_pages, dev)
     _need(slot_map, "slot_map", torch.int32, 1, dev)
     T = slot_map.shape[0]
     latent_out = _out(latent_out, "latent_out", torch.bfloat16, (T, KV4_LATENT), dev)
     rope_out = _out(rope_out, "rope_out", torch.bfloat16, (T, KV4_ROPE), dev)
-    st = _opt(status, "status", torch.int32, (1,), dev)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_kv4_read(kv_pages.data_ptr(), n_slots, slot_map.data_ptr(), T, latent_out.data_ptr(),
-                                  rope_out.data_ptr(), st, _stream_ptr(dev)))
+    _call(lib().dsa_kv4_read, dev, kv_pages.data_ptr(), n_slots, slot_map.data_ptr(), T, latent_out.data_ptr(),
+          rope_out.data_ptr(), _opt(status, "status", torch.int32, (1,), dev))
     return latent_out, rope_out
 
 
@@ -751,26 +758,32 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
     row's sequence (< 0: padding, left as it was); without it row t reads
     sequence t.  Returns (out (T, H, 512) bf16, lse (T, H) fp32).
     """
+    _kv4_pool(kv_pages)
     dev = kv_pages.device
-    _kv4_pool(kv_pages, dev)
     _need(q, "q", torch.bfloat16, 3, dev)
     T, H, dq = q.shape
     _need(block_table, "block_table", torch.int32, 2, dev)
     _need(idx, "idx", torch.int32, 2, dev)
     B, max_blocks = block_table.shape
+    n = idx.shape[1]
     if dq != KV4_LATENT + KV4_ROPE or idx.shape[0] != T:
         raise ValueError(f"need q (T, H, {KV4_LATENT + KV4_ROPE}) and idx (T, n)")
-    n = idx.shape[1]
     rs = _opt(row_seq, "row_seq", torch.int32, (T,), dev)
     out = _out(out, "out", torch.bfloat16, (T, H, KV4_LATENT), dev)
     lse = _out(lse, "lse", torch.float32, (T, H), dev)
-    st = _opt(status, "status", torch.int32, (1,), dev)
-    ws = _workspace(dsa_attend_kv4_workspace_bytes(T, H, n), dev, workspace)
-    with torch.cuda.device(dev):
-        _check(lib().dsa_attend_kv4(q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0], kv_pages.shape[1],
-                                    block_table.data_ptr(), B, max_blocks, rs, idx.data_ptr(), T, H, n, float(scale),
-                                    out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), st,
-                                    _stream_ptr(dev)))
+    if workspace is None:
+        # its size depends on the device's number of SMs
+        if torch.cuda.current_device() == dev.index:
+            nbytes = lib().dsa_attend_kv4_workspace_bytes(T, H, n)
+        else:
+            with torch.cuda.device(dev):
+                nbytes = lib().dsa_attend_kv4_workspace_bytes(T, H, n)
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+    _call(lib().dsa_attend_kv4, dev, q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0], kv_pages.shape[1],
+          block_table.data_ptr(), B, max_blocks, rs, idx.data_ptr(), T, H, n, float(scale), out.data_ptr(),
+          lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _opt(status, "status", torch.int32, (1,), dev))
     return out, lse
 
 

@@ -8,11 +8,16 @@
 //   out:    y in bf16, or E4M3 codes of y / scale with scale = max|y| / 448
 //
 // in one pass: 256 bytes read and 256 (or 132) written per row, so HBM bounds
-// it.  A row is 16 lanes of 16 bytes; its statistics are four shuffles.  The
-// angles of a token are shared by all its rows: one warp of the block forms
-// them (turns = position * inv_freq / 2 pi in fp64, since fp32 has no digits
-// left of the fraction of a turn at positions near 10^6; the fraction is then
-// exact enough for fp32 sincospi) while the rows' loads are in flight.
+// it.  A row is 8 lanes of two 8-value chunks, chosen so that both members of
+// every rotated pair are in one lane (lane l < rot / 16 of the half-split form
+// holds chunks l and l + rot / 16); statistics are three shuffles.  The angles
+// of a token are shared by all its rows: a block forms those of its tokens
+// (turns = position * inv_freq / 2 pi in fp64, since fp32 has no digits left
+// of the fraction of a turn at positions near 10^6; the fraction is then exact
+// enough for fp32 sincospi), and a lane keeps its angles and weights in
+// registers over the rows: read per row, they and the partners' shuffles made
+// the L1 pipe the bound (86%, 163 us for 16384 tokens of 64 heads; now 115 us,
+// 4.7 TB/s).
 // Statistics, rotation and scales are fp32; the store rounds once.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -27,188 +32,235 @@ namespace dsa {
 namespace {
 
 constexpr int kPrepThreads = 256;
-constexpr int kPrepRows = kPrepThreads / 16;  // rows in flight per step
-constexpr int kW = 128;                       // row width
+constexpr int kPrepRows = kPrepThreads / 8;  // rows in flight per step
+constexpr int kW = 128;                      // row width
 
-__device__ __forceinline__ float sum16(float v) {
+__device__ __forceinline__ float sum8(float v) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o, 16);
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o, 8);
   return v;
 }
-__device__ __forceinline__ float max16(float v) {
+__device__ __forceinline__ float max8(float v) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o, 16));
+  for (int o = 4; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o, 8));
   return v;
 }
 
-struct RowOut {
-  uint4 bf16;    // 8 values
-  uint2 e4m3;    // 8 codes
-  float scale;
+// The two 8-value chunks of a row that lane l of 8 holds.
+struct Chunks {
+  int a, b;
 };
+__device__ __forceinline__ Chunks chunks_of(const PrepareParams& p, bool interleaved, int l) {
+  const int half = p.rot >> 4;  // chunks of half the rotated dimensions
+  if (interleaved || l >= half) return {2 * l, 2 * l + 1};  // past the pairs: 2 half + 2 (l - half)
+  return {l, l + half};
+}
 
-// Norm and rotation of one row held as 8 values per lane (dimensions
-// 8 l .. 8 l + 7 of lane l of 16).  All 32 lanes of the warp call it.
-template <bool FP8>
-__device__ __forceinline__ RowOut prepare_row(const uint4 raw, const PrepareParams& p, int norm, const float* weight,
-                                              const float* bias, const float2* s_cs, int l) {
-  float x[8];
-  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+// Norm of a kind of rows: its weights for a lane's values, and where the bias is.
+struct NormLane {
+  int norm;
+  float w[16];
+  const float4* bias;
+};
+__device__ __forceinline__ void load_norm(NormLane& n, int norm, const float* weight, const float* bias, Chunks c) {
+  n.norm = norm;
+  n.bias = reinterpret_cast<const float4*>(bias);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int h = 0; h < 4; ++h) {
+    const float4 w = weight ? __ldg(reinterpret_cast<const float4*>(weight) + 2 * (h < 2 ? c.a : c.b) + (h & 1))
+                            : make_float4(1.f, 1.f, 1.f, 1.f);
+    n.w[4 * h] = w.x, n.w[4 * h + 1] = w.y, n.w[4 * h + 2] = w.z, n.w[4 * h + 3] = w.w;
+  }
+}
+
+struct RawRow {
+  uint4 a, b;
+};
+__device__ __forceinline__ RawRow load_row(const uint16_t* rows, int64_t row, Chunks c) {
+  const uint4* src = reinterpret_cast<const uint4*>(rows + row * kW);
+  return {__ldg(src + c.a), __ldg(src + c.b)};
+}
+
+// Norm, rotation (rotate: this lane holds pairs, cs their angles) and store of
+// one row; nothing is stored for row < 0.  All 32 lanes of the warp call it.
+template <bool FP8, bool INTER>
+__device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n, float eps, bool rotate,
+                                           const float2 (&cs)[8], Chunks c, void* out, float* scale, int64_t row, int l) {
+  float x[16];
+  const uint32_t u[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
-  if (norm != kNormNone) {
-    if (norm == kNormLayer) {
+  if (n.norm != kNormNone) {
+    if (n.norm == kNormLayer) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s += x[i];
-      const float mean = sum16(s) * (1.f / kW);
+      for (int i = 0; i < 16; ++i) s += x[i];
+      const float mean = sum8(s) * (1.f / kW);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] -= mean;
+      for (int i = 0; i < 16; ++i) x[i] -= mean;
     }
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-    const float inv = rsqrtf(fmaf(sum16(s), 1.f / kW, p.eps));
+    for (int i = 0; i < 16; ++i) s = fmaf(x[i], x[i], s);
+    const float inv = rsqrtf(fmaf(sum8(s), 1.f / kW, eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv;
-    if (weight) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(weight) + 2 * l);
-      const float4 b = __ldg(reinterpret_cast<const float4*>(weight) + 2 * l + 1);
-      x[0] *= a.x; x[1] *= a.y; x[2] *= a.z; x[3] *= a.w;
-      x[4] *= b.x; x[5] *= b.y; x[6] *= b.z; x[7] *= b.w;
-    }
-    if (bias) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(bias) + 2 * l);
-      const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + 2 * l + 1);
-      x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
-      x[4] += b.x; x[5] += b.y; x[6] += b.z; x[7] += b.w;
-    }
-  }
-  if (p.interleaved) {
-    if (8 * l < p.rot) {  // rot is a multiple of 16: a lane rotates all of its values or none
+    for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * n.w[i];
+    if (n.bias) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 cs = s_cs[4 * l + i];
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cs.x - b * cs.y;
-        x[2 * i + 1] = a * cs.y + b * cs.x;
+      for (int h = 0; h < 4; ++h) {
+        const float4 b = __ldg(n.bias + 2 * (h < 2 ? c.a : c.b) + (h & 1));
+        x[4 * h] += b.x, x[4 * h + 1] += b.y, x[4 * h + 2] += b.z, x[4 * h + 3] += b.w;
       }
     }
-  } else {
-    // dimension i pairs with i + rot / 2: the partner lane is rot / 16 away
-    const int off = p.rot >> 4;
-    const bool first = l < off, second = !first && l < 2 * off;
-    const int partner = first ? l + off : second ? l - off : l;
-    const float sign = first ? -1.f : 1.f;
+  }
+  if (rotate) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(~0u, x[i], partner, 16);
-      if (first || second) {
-        const float2 cs = s_cs[(first ? 8 * l : 8 * partner) + i];
-        x[i] = x[i] * cs.x + sign * o * cs.y;
-      }
+      float &a = INTER ? x[2 * i] : x[i], &b = INTER ? x[2 * i + 1] : x[i + 8];
+      const float r = a * cs[i].x - b * cs[i].y;
+      b = a * cs[i].y + b * cs[i].x;
+      a = r;
     }
   }
-  RowOut r{};
   if constexpr (FP8) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
-    m = max16(m);
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+    m = max8(m);
     // a row of zeros has scale 1; a scale is never subnormal, so that its
     // reciprocal is finite
-    r.scale = m > 0.f ? fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f) : 1.f;
+    const float sc = m > 0.f ? fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f) : 1.f;
     // value * (1 / scale) instead of value / scale: within two fp32 roundings
     // of the quotient, against E4M3's 2^-4
-    const float inv = __frcp_rn(r.scale);
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    r.e4m3 = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  } else {
-    uint32_t c[4];
+    const float inv = __frcp_rn(sc);
+    uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      c[i] = *reinterpret_cast<const uint32_t*>(&h);
+      const uint32_t lo =
+          __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi =
+          __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+      v[i] = lo | (hi << 16);
     }
-    r.bf16 = make_uint4(c[0], c[1], c[2], c[3]);
-  }
-  return r;
-}
-
-template <bool FP8>
-__device__ __forceinline__ void store_row(const RowOut& r, void* out, float* scale, int64_t row, int l) {
-  if constexpr (FP8) {
-    reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + row * kW)[l] = r.e4m3;
-    if (l == 0) scale[row] = r.scale;
+    if (row >= 0) {
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + row * kW);
+      dst[c.a] = make_uint2(v[0], v[1]);
+      dst[c.b] = make_uint2(v[2], v[3]);
+      if (l == 0) scale[row] = sc;
+    }
   } else {
-    reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * kW)[l] = r.bf16;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if (row >= 0) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + row * kW);
+      dst[c.a] = make_uint4(v[0], v[1], v[2], v[3]);
+      dst[c.b] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
   }
 }
 
-// Work unit = one token and U * 16 of its query heads; the unit of a token's
-// first heads also does its key.
-template <bool FP8, int U>
-__global__ void __launch_bounds__(kPrepThreads) index_prepare_kernel(const PrepareParams p) {
-  __shared__ float2 s_cs[2][kW / 2];
-  const int tid = threadIdx.x, l = tid & 15, hw = tid >> 4;
-  const int chunks = (p.H + U * kPrepRows - 1) / (U * kPrepRows);
-  const int64_t units = p.T * chunks;
-  int buf = 0;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-    const int64_t t = u / chunks;
-    const int h0 = static_cast<int>(u - t * chunks) * U * kPrepRows;
-    const int32_t pos = __ldg(p.position + t);
-    if (pos < 0) continue;  // padding (uniform over the block): nothing is written
-    uint4 raw[U], rawk = make_uint4(0u, 0u, 0u, 0u);
+// A block takes G consecutive tokens, or with G = 1 also just 32 of a token's
+// heads (blockIdx.y): it forms the tokens' angles with all threads, then each
+// group of 8 lanes walks the rows on its own, U rows of a token at a time with the
+// next U in flight.
+template <bool FP8, bool INTER, int G, int U>
+__global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_kernel(const PrepareParams p) {
+  __shared__ float2 s_cs[G][kW / 2];
+  __shared__ int s_pos[G];
+  const int tid = threadIdx.x, l = tid & 7, hw = tid >> 3;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * G;
+  const int h_lo = G > 1 ? 0 : blockIdx.y * kPrepRows, h_hi = G > 1 ? p.H : min(h_lo + kPrepRows, p.H);
+  const Chunks c = chunks_of(p, INTER, l);
+  const bool rotate = l < (p.rot >> 4);
+  // units of this block: U * 32 heads of a token
+  const int per = G > 1 ? (p.H + U * kPrepRows - 1) / (U * kPrepRows) : 1;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(G), p.T - t0));
+  RawRow next[U], rawk{};
+  auto load = [&](int g, int h0) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * kPrepRows + hw;
-      raw[i] = h < p.H ? reinterpret_cast<const uint4*>(p.q + (t * p.H + h) * kW)[l] : make_uint4(0u, 0u, 0u, 0u);
-    }
-    int64_t slot = -1;
-    if (h0 == 0 && hw < 2) {  // the key row: the first warp (its upper half repeats the lower)
-      slot = p.slot_map ? __ldg(p.slot_map + t) : t;
-      rawk = __ldg(reinterpret_cast<const uint4*>(p.k + t * kW) + l);
-    }
-    if (tid >= kPrepThreads - 64 && tid - (kPrepThreads - 64) < p.rot / 2) {
-      const int i = tid - (kPrepThreads - 64);
-      const double turns = static_cast<double>(pos) * static_cast<double>(__ldg(p.inv_freq + i)) * 0.15915494309189535;
+    for (int i = 0; i < U; ++i)
+      next[i] = load_row(p.q, (t0 + g) * p.H + min(h0 + i * kPrepRows + hw, p.H - 1), c);
+  };
+  load(0, h_lo);
+  const bool key = h_lo == 0 && (hw & ~3) < tokens;  // key row of token hw
+  int64_t slot = -1;
+  if (key) {
+    const int64_t t = t0 + min(hw, tokens - 1);
+    if (hw < tokens) slot = p.slot_map ? __ldg(p.slot_map + t) : t;
+    rawk = load_row(p.k, t, c);
+  }
+  for (int i = tid; i < tokens * (kW / 2); i += kPrepThreads) {
+    const int g = i / (kW / 2), k = i % (kW / 2);
+    const int pos = __ldg(p.position + t0 + g);
+    if (k == 0) s_pos[g] = pos;
+    if (k < p.rot / 2) {
+      const double turns = static_cast<double>(pos) * static_cast<double>(__ldg(p.inv_freq + k)) * 0.15915494309189535;
       float sn, cs;
       sincospif(2.f * static_cast<float>(turns - rint(turns)), &sn, &cs);
-      s_cs[buf][i] = make_float2(cs, sn);
+      s_cs[g][k] = make_float2(cs, sn);
     }
-    __syncthreads();  // one per unit: the other buffer's readers have passed the last one
-    if (h0 == 0 && hw < 2) {
-      const RowOut r = prepare_row<FP8>(rawk, p, p.k_norm, p.k_weight, p.k_bias, s_cs[buf], l);
-      if (hw == 0 && slot >= 0) {
-        if (slot < p.n_slots)
-          store_row<FP8>(r, p.k_out, p.k_scale, slot, l);
-        else if (l == 0 && p.status)
-          atomicOr(p.status, kErrOverflow);
-      }
-    }
+  }
+  NormLane n;
+  __syncthreads();
+  float2 cs[8];
+  auto angles = [&](int g) {
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * kPrepRows + hw;
-      if (h0 + i * kPrepRows + (hw & ~1) < p.H) {  // warp-uniform
-        const RowOut r = prepare_row<FP8>(raw[i], p, p.q_norm, p.q_weight, p.q_bias, s_cs[buf], l);
-        if (h < p.H) store_row<FP8>(r, p.q_out, p.q_scale, t * p.H + h, l);
+    for (int i = 0; i < 8; ++i) cs[i] = s_cs[g][rotate ? 8 * l + i : 0];
+  };
+  if (key) {
+    const int g = min(hw, tokens - 1);
+    load_norm(n, p.k_norm, p.k_weight, p.k_bias, c);
+    angles(g);
+    if (s_pos[g] < 0) slot = -1;  // padding
+    if (slot >= p.n_slots) {
+      if (l == 0 && p.status) atomicOr(p.status, kErrOverflow);
+      slot = -1;
+    }
+    finish_row<FP8, INTER>(rawk, n, p.eps, rotate, cs, c, p.k_out, p.k_scale, slot, l);
+  }
+  load_norm(n, p.q_norm, p.q_weight, p.q_bias, c);
+#pragma unroll 1
+  for (int u = 0, g = 0, h0 = h_lo; u < tokens * per; ++u) {
+    RawRow now[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) now[i] = next[i];
+    int g1 = g, h1 = h0 + U * kPrepRows;  // the next unit
+    if (h1 >= h_hi) {
+      h1 = h_lo;
+      ++g1;
+    }
+    if (u + 1 < tokens * per) load(g1, h1);
+    if (h0 == h_lo) angles(g);
+    if (s_pos[g] >= 0) {  // else padding: nothing is written
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int h = h0 + i * kPrepRows + hw;
+        if (h0 + i * kPrepRows + (hw & ~3) < h_hi)  // warp-uniform
+          finish_row<FP8, INTER>(now[i], n, p.eps, rotate, cs, c, p.q_out, p.q_scale, h < h_hi ? (t0 + g) * p.H + h : -1, l);
       }
     }
+    g = g1;
+    h0 = h1;
   }
 }
 
-template <bool FP8, int U>
-cudaError_t launch_u(const PrepareParams& p, int sms, cudaStream_t st) {
-  const int64_t units = p.T * ((p.H + U * kPrepRows - 1) / (U * kPrepRows));
-  const int grid = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(sms) * 8));
-  index_prepare_kernel<FP8, U><<<grid, kPrepThreads, 0, st>>>(p);
+template <bool FP8, bool INTER>
+cudaError_t launch_prepare(const PrepareParams& p, int sms, cudaStream_t st) {
+  constexpr int kGroup = 8;
+  // groups of tokens when they fill the GPU, else 32 heads a block
+  if (p.T >= static_cast<int64_t>(sms) * kGroup)
+    index_prepare_kernel<FP8, INTER, kGroup, 1>
+        <<<static_cast<unsigned>((p.T + kGroup - 1) / kGroup), kPrepThreads, 0, st>>>(p);
+  else
+    index_prepare_kernel<FP8, INTER, 1, 1><<<dim3(static_cast<unsigned>(p.T), (p.H + kPrepRows - 1) / kPrepRows),
+                                             kPrepThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -216,9 +268,8 @@ cudaError_t launch_u(const PrepareParams& p, int sms, cudaStream_t st) {
 
 cudaError_t launch_index_prepare(const PrepareParams& p, int sms, cudaStream_t st) {
   if (p.T <= 0) return cudaSuccess;
-  const bool wide = p.T >= sms;
-  if (p.fp8) return wide ? launch_u<true, 4>(p, sms, st) : launch_u<true, 1>(p, sms, st);
-  return wide ? launch_u<false, 4>(p, sms, st) : launch_u<false, 1>(p, sms, st);
+  if (p.fp8) return p.interleaved ? launch_prepare<true, true>(p, sms, st) : launch_prepare<true, false>(p, sms, st);
+  return p.interleaved ? launch_prepare<false, true>(p, sms, st) : launch_prepare<false, false>(p, sms, st);
 }
 
 }  // namespace dsa
