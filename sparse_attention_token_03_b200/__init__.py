@@ -769,7 +769,10 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
     if dq != KV4_LATENT + KV4_ROPE or idx.shape[0] != T:
         raise ValueError(f"need q (T, H, {KV4_LATENT + KV4_ROPE}) and idx (T, n)")
     rs = _opt(row_seq, "row_seq", torch.int32, (T,), dev)
-    out = _out(out, "out", torch.bfloat16, (T, H, KV4_LATENT), dev)
+    if out is None:
+        out = q.new_empty((T, H, KV4_LATENT))
+    else:
+        _arg(out, "out", torch.bfloat16, (T, H, KV4_LATENT), dev)
     lse = _out(lse, "lse", torch.float32, (T, H), dev)
     if workspace is None:
         # its size depends on the device's number of SMs
@@ -778,7 +781,7 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
         else:
             with torch.cuda.device(dev):
                 nbytes = lib().dsa_attend_kv4_workspace_bytes(T, H, n)
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        workspace = kv_pages.new_empty(max(nbytes, 256))
     else:
         _need(workspace, "workspace", torch.uint8, 1, dev)
     _call(lib().dsa_attend_kv4, dev, q.data_ptr(), kv_pages.data_ptr(), kv_pages.shape[0], kv_pages.shape[1],

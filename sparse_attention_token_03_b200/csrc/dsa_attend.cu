@@ -187,24 +187,26 @@ __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot,
 __device__ __forceinline__ constexpr int part_dim(int s) { return 2 * (s & 1) + (s >> 1); }
 
 // Query rows to shared memory as the MMA reads them (see the file's comment),
-// row by row over n_warps warps, the loads of two rows in flight.
+// row by row over the first kMmaWarp warps, the loads of all of a warp's rows
+// in flight.
 template <int NH>
 __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
-                                              int warp, int n_warps, int lane) {
-  auto live = [&](int r) { return r < NH && h0 + r < p.H; };
-  uint4 v[2][3];
-  load_query_row(v[0], p, t, h0 + warp, live(warp), lane);
-  load_query_row(v[1], p, t, h0 + warp + n_warps, live(warp + n_warps), lane);
-#pragma unroll 1
-  for (int r = warp; r < NH; r += n_warps) {
-    uint4 now[3];
+                                              int warp, int lane) {
+  constexpr int kRows = (NH + kMmaWarp - 1) / kMmaWarp;  // of a warp
+  uint4 v[kRows][3];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      now[k] = v[0][k];
-      v[0][k] = v[1][k];
+  for (int k = 0; k < kRows; ++k) {
+    const int r = warp + k * kMmaWarp;
+    load_query_row(v[k], p, t, h0 + r, r < NH && h0 + r < p.H, lane);
+  }
+#pragma unroll 1
+  for (int r = warp; r < NH; r += kMmaWarp) {
+    store_query_row(v[0], p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_dim);
+#pragma unroll
+    for (int k = 0; k + 1 < kRows; ++k) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) v[k][i] = v[k + 1][i];
     }
-    load_query_row(v[1], p, t, h0 + r + 2 * n_warps, live(r + 2 * n_warps), lane);
-    store_query_row(now, p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_dim);
   }
 }
 
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 
   if (warp <= kMmaWarp) {
     if (warp < kMmaWarp) {
-      stage_queries<NH>(p, t, h0, smem, s_c, warp, kMmaWarp, lane);
+      stage_queries<NH>(p, t, h0, smem, s_c, warp, lane);
       fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -657,25 +659,19 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         l[j].x += __shfl_xor_sync(~0u, l[j].x, o);
         l[j].y += __shfl_xor_sync(~0u, l[j].y, o);
       }
-      if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = l[j];
+      if (lane < 4) {
+        *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = l[j];
+        if (warp == 0) *reinterpret_cast<float2*>(s_c + 8 * j + 2 * lane) = make_float2(-m[j].x, -m[j].y);
+      }
     }
     named_bar_sync(1, kSoftThreads);
-    if (warp == 0 && lane < 4) {
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int col = 8 * j + 2 * lane + k;
-          const float ref = k ? -m[j].y : -m[j].x;
-          const float sum = (exch[col] + exch[NH + col]) + (exch[2 * NH + col] + exch[3 * NH + col]);
-          if (g.splits > 1) {
-            g.part_ml[item * NH + col] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
-          } else {
-            s_f[col] = sum == 0.f ? 0.f : 1.f / sum;
-            if (p.lse && h0 + col < p.H)
-              p.lse[t * p.H + h0 + col] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
-          }
-        }
+    if (tid < NH) {  // a head per thread
+      const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
+      if (g.splits > 1) {
+        g.part_ml[item * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_c[tid], sum);
+      } else {
+        s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        if (p.lse && h0 + tid < p.H) p.lse[t * p.H + h0 + tid] = sum == 0.f ? -INFINITY : (s_c[tid] + log2f(sum)) * kLn2;
       }
     }
     tc_fence_before();

@@ -153,6 +153,12 @@ __device__ __forceinline__ void ldg256(uint32_t (&r)[8], const void* p) {
       : "l"(p));
 }
 
+__device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // Division of a position (below 2^31) by the page size as a product: with s =
 // ceil(log2 d) and mul = ceil(2^(31 + s) / d) the product's error n (mul d -
 // 2^(31 + s)) / (d 2^(31 + s)) is below 1 / d, so the quotient is exact.

@@ -79,6 +79,7 @@ struct PairGrid {
   float2* part_ml;                 // [items][128]
   uint32_t* err;
   PageDiv div;
+  bool out32;                      // out is 32-byte aligned
 };
 
 // A cluster's next item with a row to work on: item k and what it stands for.
@@ -233,6 +234,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     if (lane == 0) mbar_arrive(bar(kBarTaken + i % kPairRing));
   };
 
+  // the first row's queries by all warps but the issuing ones and the list's
+  if (warp < kMma) {
+    PairItem first = it;
+    if (next_item(first, p, g, false)) {
+      const int h0 = first.hb * 2 * kHalf + rank * kHalf;
+#pragma unroll 1
+      for (int r = warp; r < kHalf; r += kMma) {
+        uint4 v[3];
+        load_query_row(v, p, first.t, h0 + r, h0 + r < p.H, lane);
+        store_query_row(v, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
+      }
+      fence_proxy_async_smem();
+    }
+    named_bar_sync(3, kMma * 32);
+  }
+
   if (warp >= kMma) {
     regs_dec<kIssueRegs>();
     if (warp == kList) {
@@ -383,29 +400,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     // ----------------------------------------------------------- queries
     regs_inc<kQRegs>();
     const int w = warp - kQ;
-    uint4 v[4][3];
     bool ok = true;
     for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
-      const int h0 = it.hb * 2 * kHalf + rank * kHalf;
-      auto load = [&](int r0) {
+      if (n > 0) {  // the first row's are staged
+        const int h0 = it.hb * 2 * kHalf + rank * kHalf;
+        uint4 v[3][3];  // three rows in flight
 #pragma unroll
-        for (int k = 0; k < 4; ++k) load_query_row(v[k], p, it.t, h0 + r0 + k, h0 + r0 + k < p.H, lane);
-      };
-      load(16 * w);
-      if (!(ok = wait(kBarQE, n + 1) && wait(kBarCE, n + 1))) break;
+        for (int k = 0; k < 3; ++k) load_query_row(v[k], p, it.t, h0 + 16 * w + k, h0 + 16 * w + k < p.H, lane);
+        if (!(ok = wait(kBarQE, n + 1) && wait(kBarCE, n + 1))) break;
 #pragma unroll 1
-      for (int r = 0;; ++r) {
-        store_query_row(v[0], p.scale, smem + kOffQ, kBlk, 16 * w + r, s_c, lane, [](int s) { return s; });
-        if (r == 15) break;
-        if ((r & 3) == 3) {
-          load(16 * w + r + 1);
-        } else {
+        for (int r = 16 * w; r < 16 * w + 16; ++r) {
+          uint4 now[3];
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
+            now[k] = v[0][k];
             v[0][k] = v[1][k];
             v[1][k] = v[2][k];
-            v[2][k] = v[3][k];
           }
+          load_query_row(v[2], p, it.t, h0 + r + 3, r < 16 * w + 13 && h0 + r + 3 < p.H, lane);
+          store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
         }
       }
       fence_proxy_async_smem();
@@ -632,9 +645,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         if (h >= p.H) {
           // no such head
         } else if (g.splits > 1) {
-          uint4* dst = reinterpret_cast<uint4*>(g.part_o + part_row * kKvLat + dim);
+          float* dst = g.part_o + part_row * kKvLat + dim;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) stg256(dst + 8 * k, o + 8 * k);
         } else {
           uint32_t b[16];
 #pragma unroll
@@ -643,9 +656,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
                 __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * f, __uint_as_float(o[2 * k + 1]) * f);
             b[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (it.t * p.H + h) * kKvLat + dim);
+          uint16_t* dst = p.out + (it.t * p.H + h) * kKvLat + dim;
+          if (g.out32) {  // whole sectors
+            stg256(dst, b);
+            stg256(dst + 16, b + 8);
+          } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<uint4*>(dst)[k] = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+          }
         }
         __syncwarp();
       }
@@ -724,7 +743,7 @@ cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int s
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PairGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(P.items), reinterpret_cast<float*>(ws + P.off_o),
              reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws),
-             page_div(p.page_size)};
+             page_div(p.page_size), reinterpret_cast<uintptr_t>(p.out) % 32 == 0};
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
