@@ -50,7 +50,7 @@ constexpr int kK = 4, kV = 12, kQ = 20, kMma = 24, kList = 25, kMmaO = 26;  // f
 constexpr int kPairThreads = 28 * 32;
 constexpr int kPairRing = 4;                      // tiles that the list warp may be ahead
 // registers per thread: 72 at launch, then shared out by warpgroup
-constexpr uint32_t kSoftRegs = 96, kKRegs = 72, kVRegs = 64, kQRegs = 80, kIssueRegs = 56;
+constexpr uint32_t kSoftRegs = 96, kKRegs = 72, kVRegs = 72, kQRegs = 64, kIssueRegs = 56;
 static_assert(kSoftRegs * 128 + kKRegs * 256 + kVRegs * 256 + kQRegs * 128 + kIssueRegs * 128 <= 72 * kPairThreads,
               "register pool");
 
@@ -207,9 +207,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     mbar_init(bar(kBarSE + 1), 8);
     mbar_init(bar(kBarP), 8);
     mbar_init(bar(kBarO), 1);
-    mbar_init(bar(kBarQF), 8);
+    mbar_init(bar(kBarQF), 24);  // Q and V warps
     mbar_init(bar(kBarQE), 1);
-    mbar_init(bar(kBarCF), 4);
+    mbar_init(bar(kBarCF), 12);
     mbar_init(bar(kBarCE), 4);
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarDrain + 1), 1);
@@ -232,6 +232,36 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   auto taken = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTaken + i % kPairRing));
+  };
+
+  // Queries of rows r0 .. r0 + rows - 1 of this block for its item number n (the
+  // first item's are staged below), and the word that they are there.
+  auto stage = [&](const PairItem& item, int n, int r0, int rows) {
+    if (n > 0) {
+      const int h0 = item.hb * 2 * kHalf + rank * kHalf;
+      uint4 v[2][3];  // two rows in flight
+      load_query_row(v[0], p, item.t, h0 + r0, h0 + r0 < p.H, lane);
+      load_query_row(v[1], p, item.t, h0 + r0 + 1, h0 + r0 + 1 < p.H, lane);
+      if (!wait(kBarQE, n + 1) || !wait(kBarCE, n + 1)) return false;
+#pragma unroll 1
+      for (int r = r0; r < r0 + rows; ++r) {
+        uint4 now[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          now[k] = v[0][k];
+          v[0][k] = v[1][k];
+        }
+        load_query_row(v[1], p, item.t, h0 + r + 2, r + 2 < r0 + rows && h0 + r + 2 < p.H, lane);
+        store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
+      }
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bar(kBarCF));
+      arrive_cluster(in_first(bar(kBarQF)));
+    }
+    return true;
   };
 
   // the first row's queries by all warps but the issuing ones and the list's
@@ -398,44 +428,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     }
   } else if (warp >= kQ) {
     // ----------------------------------------------------------- queries
-    regs_inc<kQRegs>();
-    const int w = warp - kQ;
+    regs_dec<kQRegs>();
     bool ok = true;
-    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
-      if (n > 0) {  // the first row's are staged
-        const int h0 = it.hb * 2 * kHalf + rank * kHalf;
-        uint4 v[3][3];  // three rows in flight
-#pragma unroll
-        for (int k = 0; k < 3; ++k) load_query_row(v[k], p, it.t, h0 + 16 * w + k, h0 + 16 * w + k < p.H, lane);
-        if (!(ok = wait(kBarQE, n + 1) && wait(kBarCE, n + 1))) break;
-#pragma unroll 1
-        for (int r = 16 * w; r < 16 * w + 16; ++r) {
-          uint4 now[3];
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            now[k] = v[0][k];
-            v[0][k] = v[1][k];
-            v[1][k] = v[2][k];
-          }
-          load_query_row(v[2], p, it.t, h0 + r + 3, r < 16 * w + 13 && h0 + r + 3 < p.H, lane);
-          store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(kBarCF));
-        arrive_cluster(in_first(bar(kBarQF)));
-      }
-    }
+    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) ok = stage(it, n, 8 * (warp - kQ), 8);
   } else if (warp >= kV) {
     // ----------------------------------------------------------------- V
-    regs_dec<kVRegs>();
     const int lw = warp - kV, key = lw * 16 + (lane & 15), half = lane >> 4, u = lw >> 1;
     const uint32_t row = sV + 2 * half * kVBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
     const uint32_t full = in_first(bar(kBarVF + u));
     RawLatent raw;
-    for (int i = -1;; ++i) {  // loads of tile i + 1, then tile i to shared memory
+    int meta = 0, n = 0;
+    bool ok = next_item(it, p, g, false) && stage(it, n, 32 + 4 * lw, 4);
+    for (int i = -1; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
       if (!listed(i + 1)) break;
       RawLatent next;
       const int m = s_meta[(i + 1) % kPairRing];
@@ -451,9 +455,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_cluster(full);
+        if (meta & kLast) {  // half of the next row's queries: V has the time, K has not
+          it.k += gridDim.x >> 1;
+          if (next_item(it, p, g, false)) ok = stage(it, ++n, 32 + 4 * lw, 4);
+        }
       }
       if (m & kStop) break;
       raw = next;
+      meta = m;
     }
   } else if (warp >= kK) {
     // ----------------------------------------------------------------- K
