@@ -31,7 +31,7 @@
 // O^T's product over a part frees it, so the next tile's decoding and scores
 // follow part by part.  The gathering warps are two groups of eight; each
 // lane decodes 64 consecutive dimensions of its key, 32 for each of its
-// group's two parts (part_dim gives the order; staged queries and output rows
+// group's two parts (dim_of gives the order; staged queries and output rows
 // follow it).
 //
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
@@ -170,8 +170,8 @@ struct RawKey {
 __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot, bool live, int part, int group) {
   if (live) {
     const uint8_t* e = kv + static_cast<int64_t>(slot) * kKvEntry;
-    ldg256(r.code, e + part * 64 + group * 32);
-    r.scale = __ldg(reinterpret_cast<const uint32_t*>(e + kKvScaleOff + part * 8 + group * 4));
+    ldg256(r.code, e + group * 128 + part * 32);
+    r.scale = __ldg(reinterpret_cast<const uint32_t*>(e + kKvScaleOff + group * 16 + part * 4));
     r.rope = __ldg(reinterpret_cast<const uint4*>(e + kKvRopeOff + (2 * part + group) * 16));
   } else {
     // behind the last key: zeros, so that no bit pattern of the pool meets a zero weight
@@ -182,9 +182,11 @@ __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot,
   }
 }
 
-// Hand-over part s of a tile and its latent dimensions: position 128 s + 32 p
-// + r holds dimension 128 p + 32 part_dim(s) + r (the map is its own inverse).
-__device__ __forceinline__ constexpr int part_dim(int s) { return 2 * (s & 1) + (s >> 1); }
+// Quarter p of hand-over part s of a tile holds latent dimensions 256 (s % 2)
+// + 64 p + 32 (s / 2) .. + 31: a group's four lanes of a key load 128
+// contiguous bytes of codes and decode 32 dimensions of each of its parts.
+__device__ __forceinline__ constexpr int part_of(int hi, int lo) { return hi + 2 * lo; }
+__device__ __forceinline__ constexpr int dim_of(int s, int p) { return 256 * (s & 1) + 64 * p + 32 * (s >> 1); }
 
 // Query rows to shared memory as the MMA reads them (see the file's comment),
 // row by row over the first kMmaWarp warps, the loads of all of a warp's rows
@@ -201,7 +203,7 @@ __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, 
   }
 #pragma unroll 1
   for (int r = warp; r < NH; r += kMmaWarp) {
-    store_query_row(v[0], p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_dim);
+    store_query_row(v[0], p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_of);
 #pragma unroll
     for (int k = 0; k + 1 < kRows; ++k) {
 #pragma unroll
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
               make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
                           __uint_as_float(o[4 * j + 3]));
       } else {
-        const int dim = 128 * pq + 32 * part_dim(s) + 16 * half + (lane & 8);
+        const int dim = dim_of(s, pq) + 16 * half + (lane & 8);
 #pragma unroll
         for (int j = 0; j < NH / 8; j += 2) {
           uint32_t v[4];
@@ -737,7 +739,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
   __syncthreads();
   if (threadIdx.x < 128 && h0 + (threadIdx.x >> 4) < p.H) {  // 16 bytes: 8 dimensions of a head
     const int h = threadIdx.x >> 4, c = threadIdx.x & 15;
-    *reinterpret_cast<uint4*>(p.out + (t * p.H + h0 + h) * kKvLat + 128 * (c >> 2) + 32 * part_dim(s) + 8 * (c & 3)) =
+    *reinterpret_cast<uint4*>(p.out + (t * p.H + h0 + h) * kKvLat + dim_of(s, c >> 2) + 8 * (c & 3)) =
         *reinterpret_cast<const uint4*>(&s_o[h][8 * c]);
   }
 }

@@ -212,12 +212,14 @@ __device__ __forceinline__ void load_query_row(uint4 (&v)[3], const AttendParams
 
 // Row r of the staged queries: latent parts to fp16 and rotary parts to bf16,
 // both times the power of two that puts the row's largest magnitude in [2^14,
-// 2^15); s_c[r] takes the factor of its scores in log2 units.  Column block 2
-// order(s) + p / 2 (of q_block bytes) holds latent dimensions 128 p + 32 s ..
-// + 31 in its half p % 2; block 8 the rotary ones.
-template <typename Order>
+// 2^15); s_c[r] takes the factor of its scores in log2 units.  Column blocks
+// 2 s and 2 s + 1 (of q_block bytes) hold hand-over part s: the 32 dimensions
+// of quarter p of it are the latent dimensions 256 hi + 64 p + 32 lo .. + 31
+// with s = part_of(hi, lo); block 8 holds the rotary ones.  Few instructions
+// rather than fast ones: this runs once a row, from a cold instruction cache.
+template <typename PartOf>
 __device__ __forceinline__ void store_query_row(const uint4 (&v)[3], float scale, uint8_t* smem, uint32_t q_block, int r,
-                                                float* s_c, int lane, Order order) {
+                                                float* s_c, int lane, PartOf part_of) {
   uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -228,27 +230,24 @@ __device__ __forceinline__ void store_query_row(const uint4 (&v)[3], float scale
   const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
   const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
   if (lane == 0) s_c[r] = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const int c = lane + 32 * i;
-    if (c >= kQChunks) continue;
+  uint4 now = v[0], next = v[1], last = v[2];
+#pragma unroll 1
+  for (int c = lane; c < kQChunks; c += 32) {
     const bool rotary = c >= kKvLat / 8;
-    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t o[4];
+    uint32_t u[4] = {now.x, now.y, now.z, now.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
-      if (!rotary) {
-        const __half2 h = __floats2half2_rn(a, b);
-        o[k] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        o[k] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+      const __half2 h = __floats2half2_rn(a, b);
+      const __nv_bfloat162 f = __floats2bfloat162_rn(a, b);
+      u[k] = rotary ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
     }
-    const int blk = rotary ? 8 : 2 * order((c >> 2) & 3) + (c >> 5);
-    const int at = rotary ? c & 7 : ((c >> 2) & 4) + (c & 3);
-    *reinterpret_cast<uint4*>(smem + blk * q_block + r * 128 + ((at ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    const int p = (c >> 3) & 3;
+    const int blk = rotary ? 8 : 2 * part_of(c >> 5, (c >> 2) & 1) + (p >> 1);
+    const int at = rotary ? c & 7 : 4 * (p & 1) + (c & 3);
+    *reinterpret_cast<uint4*>(smem + blk * q_block + r * 128 + ((at ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
+    now = next;
+    next = last;
   }
 }
 

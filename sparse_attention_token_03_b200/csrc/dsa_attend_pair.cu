@@ -134,20 +134,23 @@ __device__ __forceinline__ bool heads_bar_or(int id, bool v) {
   return r != 0;
 }
 
-// 128 latent dimensions of a key: 64 bytes of codes and eight scales.
+// 128 latent dimensions of a key, two runs of 64: codes and scales.
 struct RawLatent {
   uint32_t code[16];
   uint64_t scale;
 };
-__device__ __forceinline__ void load_latent(RawLatent& r, const uint8_t* entry, int part) {
-  uint32_t a[8], b[8];
-  ldg256(a, entry + part * 64);
-  ldg256(b, entry + part * 64 + 32);
-  r.scale = __ldg(reinterpret_cast<const unsigned long long*>(entry + kKvScaleOff + part * 8));
+// Runs number a and b of the entry's eight.
+__device__ __forceinline__ void load_latent(RawLatent& r, const uint8_t* entry, int a, int b) {
+  uint32_t x[8], y[8];
+  ldg256(x, entry + a * 32);
+  ldg256(y, entry + b * 32);
+  const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(entry + kKvScaleOff) + a);
+  const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(entry + kKvScaleOff) + b);
+  r.scale = static_cast<uint64_t>(hi) << 32 | lo;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    r.code[i] = a[i];
-    r.code[8 + i] = b[i];
+    r.code[i] = x[i];
+    r.code[8 + i] = y[i];
   }
 }
 __device__ __forceinline__ void zero_latent(RawLatent& r) {
@@ -155,6 +158,11 @@ __device__ __forceinline__ void zero_latent(RawLatent& r) {
   for (int i = 0; i < 16; ++i) r.code[i] = 0u;
   r.scale = 0u;
 }
+// Quarter p of hand-over part s of K holds latent dimensions 256 (s / 2) + 64 p
+// + 32 (s % 2) .. + 31, so that the four lanes of a key load 128 contiguous
+// bytes at a time.
+__device__ __forceinline__ constexpr int part_of(int hi, int lo) { return 2 * hi + lo; }
+
 // Decodes the next 32 dimensions to four chunks of 16 bytes, chunk k at dst +
 // ((k ^ swz) << 4), and moves the rest down (a loop over all 128 keeps the
 // code small, which counts here: the roles' loops together pass the size of
@@ -239,7 +247,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   auto stage = [&](const PairItem& item, int n, int r0, int rows) {
     if (n > 0) {
       const int h0 = item.hb * 2 * kHalf + rank * kHalf;
-      uint4 v[2][3];  // two rows in flight
+      // all rows on their way to L2 during the wait, two at a time from there
+      const char* src = reinterpret_cast<const char*>(p.q + (item.t * p.H + h0 + r0) * kKvQ);
+      for (int b = lane * 128; b < min(rows, p.H - h0 - r0) * 2 * kKvQ; b += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b));
+      uint4 v[2][3];
       load_query_row(v[0], p, item.t, h0 + r0, h0 + r0 < p.H, lane);
       load_query_row(v[1], p, item.t, h0 + r0 + 1, h0 + r0 + 1 < p.H, lane);
       if (!wait(kBarQE, n + 1) || !wait(kBarCE, n + 1)) return false;
@@ -252,7 +264,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
           v[0][k] = v[1][k];
         }
         load_query_row(v[1], p, item.t, h0 + r + 2, r + 2 < r0 + rows && h0 + r + 2 < p.H, lane);
-        store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
+        store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, part_of);
       }
       fence_proxy_async_smem();
     }
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       for (int r = warp; r < kHalf; r += kMma) {
         uint4 v[3];
         load_query_row(v, p, first.t, h0 + r, h0 + r < p.H, lane);
-        store_query_row(v, p.scale, smem + kOffQ, kBlk, r, s_c, lane, [](int s) { return s; });
+        store_query_row(v, p.scale, smem + kOffQ, kBlk, r, s_c, lane, part_of);
       }
       fence_proxy_async_smem();
     }
@@ -434,7 +446,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   } else if (warp >= kV) {
     // ----------------------------------------------------------------- V
     const int lw = warp - kV, key = lw * 16 + (lane & 15), half = lane >> 4, u = lw >> 1;
-    const uint32_t row = sV + 2 * half * kVBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
+    const uint32_t row = sV + half * kVBlk + key * 128, sw = static_cast<uint32_t>(key & 7);
     const uint32_t full = in_first(bar(kBarVF + u));
     RawLatent raw;
     int meta = 0, n = 0;
@@ -444,14 +456,15 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       RawLatent next;
       const int m = s_meta[(i + 1) % kPairRing];
       if (key < (m & 0xFFFF))
-        load_latent(next, p.kv + static_cast<int64_t>(s_ring[(i + 1) % kPairRing * kTile + key]) * kKvEntry, 2 * rank + half);
+        load_latent(next, p.kv + static_cast<int64_t>(s_ring[(i + 1) % kPairRing * kTile + key]) * kKvEntry, 4 * rank + half,
+                    4 * rank + 2 + half);
       else
         zero_latent(next);
       taken(i + 1);
       if (i >= 0) {
         if (!wait(kBarVE + u, i + 1)) break;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) decode_step(raw, row + (s >> 1) * kVBlk + ((((4 * s) ^ sw) & 4) << 4), sw & 3);
+        for (int s = 0; s < 4; ++s) decode_step(raw, row + (s & 2) * kVBlk + ((((4 * s) ^ sw) & 4) << 4), sw & 3);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_cluster(full);
@@ -480,7 +493,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       if (rank * kHalf + key < (m & 0xFFFF)) {
         const uint8_t* e =
             p.kv + static_cast<int64_t>(s_ring[(i + 1) % kPairRing * kTile + rank * kHalf + key]) * kKvEntry;
-        load_latent(next, e, part);
+        load_latent(next, e, part, 4 + part);
         ldg256(next_rope, e + kKvRopeOff + part * 32);
       } else {
         zero_latent(next);
