@@ -1,0 +1,100 @@
+"""Attention over selected keys where blocks take several rows, lists split
+into parts, pages have odd sizes and calls overlap (formulas and tolerances:
+test_gpu_attend.py, serve_ref.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_token_03_b200 as dsa
+from tests import serve_ref as ref
+from tests.test_gpu_attend import SCALE, check, gpu, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H", [16, 64, 128])
+@pytest.mark.parametrize("where", ["first", "last"])
+def test_low_scores_with_empty_parts(H, where):
+    # one row's list splits over many blocks; all scores are near -600 and all
+    # but one part are empty, so a part without keys must not set the reference
+    x = make(1, H, 2048, ctx=2100, seed=H)
+    lat = np.full((x["entries"].shape[0], 512), 2.0)
+    x["entries"] = ref.kv4_encode(lat, ref.bf16_bits(np.random.default_rng(H).standard_normal((lat.shape[0], 64))))
+    q = ref.bf16_f64(x["q"])
+    q[..., :512] = -8.0
+    x["q"] = ref.bf16_bits(q)
+    if where == "first":
+        x["idx"][:, 40:] = -1
+    else:
+        x["idx"][:, :-40] = -1
+    out, lse = check(x)
+    assert (lse < -400).all() and (out.abs() > 1).all()
+
+
+@pytest.mark.parametrize("page", [1, 7, 63, 1000])
+@pytest.mark.parametrize("H", [16, 128])
+def test_page_sizes(page, H):
+    check(make(4, H, 150, B=2, ctx=333, page=page, seed=page + H, fill="holes"))
+
+
+@pytest.mark.parametrize("T,H", [(160, 65), (225, 128), (90, 200), (300, 64)])
+def test_more_rows_than_blocks(T, H):
+    # each block works through several rows: short, long and empty lists, and
+    # padding rows between them
+    x = make(T, H, 300, B=5, ctx=700, seed=T, fill="ragged")
+    x["row_seq"][::7] = -1
+    x["idx"][11::13] = -1
+    g = gpu(x)
+    out = torch.full((T, H, 512), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, H), 5.0, device="cuda")
+    dsa.dsa_attend_kv4(scale=SCALE, out=out, lse=lse, **g)
+    want = ref.attend(ref.bf16_f64(x["q"]), x["entries"], x["table"], 64, x["row_seq"], x["idx"], SCALE)
+    keep = x["row_seq"] >= 0
+    ref.check_attend(out.double().cpu().numpy()[keep], lse.double().cpu().numpy()[keep], [w[keep] for w in want])
+    assert (out[~torch.from_numpy(keep)] == 5).all() and (lse[~torch.from_numpy(keep)] == 5).all()
+
+
+@pytest.mark.parametrize("H", [32, 128])
+def test_only_padding(H):
+    x = make(4, H, 40, seed=1)
+    x["row_seq"][:] = -1
+    out = torch.full((4, H, 512), 5.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_attend_kv4(scale=SCALE, out=out, **gpu(x))
+    assert (out == 5).all()
+
+
+@pytest.mark.parametrize("T,H", [(3, 128), (200, 128), (3, 24), (200, 24)])
+def test_output_on_16_byte_boundaries(T, H):
+    x = make(T, H, 90, B=2, seed=T + H)
+    out = torch.full((T * H * 512 + 16,), 5.0, dtype=torch.bfloat16, device="cuda")
+    view = out[8:-8].view(T, H, 512)
+    assert view.data_ptr() % 32 == 16
+    dsa.dsa_attend_kv4(scale=SCALE, out=view, **gpu(x))
+    want = dsa.dsa_attend_kv4(scale=SCALE, **gpu(x))
+    assert torch.equal(view, want[0]) and (out[:8] == 5).all() and (out[-8:] == 5).all()
+
+
+def test_both_kinds_of_blocks_at_once():
+    # few and many heads on two streams, in flight together
+    xs = [make(150, 128, 300, B=2, ctx=600, seed=21), make(300, 16, 300, B=2, ctx=600, seed=22)]
+    gs, alone = [gpu(x) for x in xs], []
+    for x, g in zip(xs, gs):
+        alone.append(dsa.dsa_attend_kv4(scale=SCALE, **g))
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for k in range(2):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(dsa.dsa_attend_kv4(scale=SCALE, **gs[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for o, l in got[k]:
+            assert torch.equal(o, alone[k][0]) and torch.equal(l, alone[k][1])
+
+
+def test_a_list_of_one_key_many_times():
+    x = make(2, 128, 700, seed=23)
+    x["idx"][:] = 17
+    check(x)

@@ -173,3 +173,20 @@ def test_prepare_replays_in_a_graph():
         graph.replay()
         want = call(x, False, False)
         assert np.array_equal(q_out.double().cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,rot,norms", [(1203, 5, 64, 1), (1190, 33, 32, 0), (1185, 64, 128, 2), (1184, 1, 16, 1)])
+def test_prepare_many_tokens(T, H, rot, norms, interleaved, fp8):
+    # enough tokens that a block takes a group of them; the last group is short
+    # and padding rows end inside a group
+    test_prepare(T, H, rot, norms, interleaved, fp8)
+
+
+def test_prepare_many_tokens_in_place():
+    x = make(1300, 20, 64, "rms", "rms", seed=31, pad=7)
+    a = call(x, False, False)
+    b = call(x, False, False, q_out="in place")
+    assert np.array_equal(a[0][:-7], b[0][:-7]) and np.array_equal(a[1], b[1])
+    assert np.array_equal(b[0][-7:], ref.bf16_f64(x["q"])[-7:])
