@@ -371,10 +371,13 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         uint32_t ready = 0;
         if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, g.err)) || s_n[b] == 0) break;
         if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort, g.err))) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
-          if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, g.err))) break;
-          tc_fence_after();
+          if (!((ready >> s) & 1u)) {
+            if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, g.err))) break;
+            tc_fence_after();
+          }
           const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)

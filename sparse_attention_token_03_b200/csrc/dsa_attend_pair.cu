@@ -374,8 +374,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         uint32_t ready = 0;  // of the four parts
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
-          if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
-          tc_fence_after();
+          if (!((ready >> s) & 1u)) {
+            if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
+            tc_fence_after();
+          }
           const uint64_t q0 = dQ + (2 * s * kBlk >> 4), k0 = dK + (2 * s * kBlk >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
@@ -416,10 +418,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         const uint32_t mine = bar(lane == 4 ? kBarP : kBarVF + (lane & 3));
         uint32_t ready = 0;
         if (!wait_any(ready, 4, lane < 5, mine, i & 1, s_abort, g.err)) break;
+        tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
-          if (!(ok = wait_any(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
-          tc_fence_after();
+          if (!((ready >> u) & 1u)) {
+            if (!(ok = wait_any(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
+            tc_fence_after();
+          }
           const uint64_t a0 = dP + (((u >> 1) * kBlk + 64 * (u & 1)) >> 4), b0 = dV + (2 * u * 2048 >> 4);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk) {
