@@ -61,8 +61,9 @@ constexpr int kParts = kKvLat / 128;             // hand-over parts of a tile bu
 constexpr uint32_t kBlockBytes = kKt * 128;      // one column block
 constexpr uint32_t kTileBytes = kBlocks * kBlockBytes;
 constexpr int kSoftWarps = 4, kLoadWarps = 16;   // loaders: two groups of 8 warps, 8 keys a warp
-constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1, kMmaOWarp = kMmaWarp + 2;
-constexpr int kAttThreads = (kMmaWarp + 4) * 32;       // whole warpgroups: one warp of the last one idles
+constexpr int kMmaWarp = kSoftWarps + kLoadWarps, kListWarp = kMmaWarp + 1, kMmaOWarp = kMmaWarp + 2,
+              kMmaOddWarp = kMmaWarp + 3;
+constexpr int kAttThreads = (kMmaWarp + 4) * 32;
 constexpr int kWorkThreads = (kSoftWarps + kLoadWarps) * 32;
 // registers per thread: 80 at launch, then shared out by warpgroup
 constexpr uint32_t kSoftRegs = 136, kLoadRegs = 72, kIssueRegs = 56;
@@ -81,8 +82,8 @@ struct AttSmem {
   static constexpr uint32_t off_ring = off_f + NH * 4;   // pool rows of the next tiles' keys
   static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // keys of each ring tile, then of each buffer
   static constexpr uint32_t off_bars = off_count + (kRing + 2) * 4;
-  // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], weights, output, drain [2]
-  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 4 + 4;
+  // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], weights, output, drain [3]
+  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 4 + 5;
   static constexpr uint32_t off_misc = off_bars + 8 * n_bars;
   static constexpr uint32_t bytes = off_misc + 16;
   static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     mbar_init(bar_read(1), kSoftWarps);
     mbar_init(bar_drain, 1);
     mbar_init(bar_drain + 8, 1);
+    mbar_init(bar_drain + 16, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(bar_listed(r), 1);
       mbar_init(bar_taken(r), kLoadWarps);
@@ -356,14 +358,17 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       if (ok && keys > 0) turn();
       if (ok) publish();
       if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kMmaOddWarp) {
       // -------------------------------------------------- MMAs of the scores
+      // One warp for each tile buffer: 36 MMAs take a warp longer to issue than
+      // the tensor core to run when the heads are few.
       constexpr uint32_t tmem = 0;
       constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0, 0), kIdR = idesc_att(64, NH, 1, 0, 0);
       const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ);
       const uint32_t leader = elect_one();
       bool ok = true;
-      for (int i = 0; ok; ++i) {
+      const uint32_t drain = warp == kMmaWarp ? bar_drain : bar_drain + 16;
+      for (int i = warp == kMmaWarp ? 0 : 1; ok; i += 2) {
         const int b = i & 1;
         const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
         // lane by lane: the tile's four parts, and that the scores of tile i - 2 are read
@@ -393,9 +398,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         }
       }
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
-      commit_if(leader, bar_drain);
+      commit_if(leader, drain);
       int unused = 0;
-      wait_bar(bar_drain, 0, &unused, g.err);
+      wait_bar(drain, 0, &unused, g.err);
       __syncwarp();
     } else if (warp == kMmaOWarp) {
       // ------------------------------------------------- MMAs of the outputs
@@ -431,8 +436,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     const int key = lw * 8 + (lane & 7), part = lane >> 3;
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
     RawKey raw;
-    int n_keys = 0, i = -1;
-    for (bool ok = true; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
+    int n_keys = 0, nt = -1;  // nt: tiles, once the end is known
+    bool ok = true;
+    for (int i = -1; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
       RawKey next;
       int n_next = 0;
       if (i < 0 || n_keys > 0) {
@@ -472,7 +478,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           if (lane == 0) mbar_arrive(bar_full(b, s));
           if (n_keys == 0) break;  // the end of the list: part 0 alone carries it
         }
-        if (n_keys == 0) break;
+        if (n_keys == 0) {  // told to both buffers' readers
+          if (nt >= 0) break;
+          nt = i;
+        }
       }
       raw = next;
       n_keys = n_next;
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       uint32_t o[NH / 2];
-      if (i > 0) {
+      if (nt > 0) {
         tmem_ld_tile(tmem + kTmemO + s * NH + (static_cast<uint32_t>(pq * 32 + half * 16) << 16), o);
         tmem_wait_ld();
       } else {
