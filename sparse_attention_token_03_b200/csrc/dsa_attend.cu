@@ -4,9 +4,10 @@
 //   z(t,h,j) = scale * (q(t,h) . [latent_j, rotary_j])
 //   out(t,h) = sum_j softmax_j(z) latent_j,   lse(t,h) = log sum_j exp z
 //
-// A block works on one row, up to 64 of its heads and a range of its list, in
-// tiles of 64 keys.  Both products have the keys' or the latent dimensions as
-// the MMA's rows and the heads as its columns,
+// A block works on one row, up to 64 heads and a range of the row's list, in
+// tiles of 64 keys (dsa_attend_pair.cu has the kernel for more heads).  Both
+// products have the keys' or the latent dimensions as the MMA's rows and the
+// heads as its columns,
 //
 //   S^T [64 keys x heads]  = K [64 x 576] Q^T         (M = 64,  36 K steps)
 //   O^T [512 x heads]     += V^T [512 x 64] P^T       (M = 128, 4 x 4 K steps)
@@ -17,15 +18,16 @@
 // blocks of [64 keys][128 bytes] with the 128-byte swizzle, read K-major for
 // S and M-major for O.
 //
-//   warps 0-3    softmax: S^T from TMEM, exp2, P^T to shared memory
-//   warps 4-19   gather and decode: eight lanes per key load its 416 bytes one
-//                tile ahead into registers, E2M1 -> fp16 times the block scale
-//                (exact), and store the swizzled tile, two tile buffers; at
-//                the end O^T from TMEM through shared memory to the output
-//   warp 20      issues the MMAs
-//   warp 21      reads the list and the block table and packs the pool rows of
-//                the entries that name a key into tiles, so that gaps and
-//                short lists cost no tiles
+//   warps 0-3     softmax: S^T from TMEM, exp2, P^T to shared memory
+//   warps 4-19    gather and decode: eight lanes per key load its 416 bytes one
+//                 tile ahead into registers, E2M1 -> fp16 times the block scale
+//                 (exact), and store the swizzled tile, two tile buffers; at
+//                 the end O^T from TMEM through shared memory to the output
+//   warps 20, 23  issue the MMAs of S, one for each tile buffer
+//   warp 22       issues the MMAs of O
+//   warp 21       reads the list and the block table and packs the pool rows of
+//                 the entries that name a key into tiles, so that gaps and
+//                 short lists cost no tiles
 //
 // A tile buffer is handed over in four parts of 128 dimensions, both ways:
 // O^T's product over a part frees it, so the next tile's decoding and scores
@@ -34,16 +36,23 @@
 // group's two parts (dim_of gives the order; staged queries and output rows
 // follow it).
 //
+// What bounds it: with 64 heads the 128-byte wavefronts of shared memory, some
+// 3000 a tile (operands of the MMAs 1920, decoding 576, the rest P, slots and
+// conflicts) in 4200 cycles, the block's start and end included, against 1970
+// cycles of MMAs; with few heads the way round a tile buffer (decode, S,
+// softmax, O: some 5500 cycles for two tiles in flight).  999 rows of 64 heads
+// and 2048 entries: 535 us, 533 TFLOP/s; 148 rows of 16 heads: 64 us.
+//
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
 // bits, 2^-10 .. 2688).  Queries go to fp16 too, each row scaled by the power
 // of two that puts its largest magnitude in [2^14, 2^15): bf16's 8 bits fit,
 // and only values below 2^-28 of that maximum round, to 2^-39 of it.  The
 // rotary parts multiply as bf16 (same power of two, exact).  P is fp16, 2^-11
 // relative (bf16's 2^-8 would double the output's error).  exp2 is taken
-// relative to a reference per head that follows the running maximum from at
-// most 2^8 below, so P stays at most 256 and O^T in TMEM is rescaled only
-// when a tile passes that, which ordinary score distributions do in the first
-// tile alone.  Scores, sums and O^T are fp32.
+// relative to a reference per head, the maximum of the first tile, that moves
+// to the running maximum when a score passes it by 2^8, so P stays at most 256
+// and O^T in TMEM is rescaled only then, which ordinary score distributions
+// never need.  Scores, sums and O^T are fp32.
 //
 // Few rows: the list is split over blocks, each writes its fp32 O and (m, l),
 // and a second kernel joins them.

@@ -11,29 +11,34 @@
 // 256 c .. 256 c + 255), and gets the scores and outputs of its heads: TMEM
 // lanes 0-63 the first half of a product's columns, lanes 64-127 the second.
 //
-// What bounds it is shared memory: with 64 heads per block on their own, a
-// 64-key tile moves 2560 wavefronts of 128 bytes (operands 1920, decoding
-// 640) against 1972 cycles of MMAs; here a 128-key tile of 128 heads moves
-// 3136 per block (operands 1920, decoding 1088, P 128) against 36 x 53 + 16 x
-// 65 = 2940 cycles, for twice the products.
+// Why pairs: shared memory's 128-byte wavefronts bound these kernels.  64 heads
+// of a block on their own move some 3000 for 64 keys; here 128 keys of 128
+// heads move 3900 per block (operands of the MMAs 1920, decoding 1088, P 128,
+// the rest slots, queries and conflicts) for twice the products, in 5250
+// cycles against 36 x 53 + 16 x 65 = 2950 of MMAs.  2048 rows of 128 heads and
+// 2048 entries: 1.29 ms, 905 TFLOP/s (64-head blocks: 2.14 ms).
 //
 //   warps 0-3    softmax and output; a thread has one head and half of the keys
 //                (output dimensions), so maxima and sums need no shuffles
 //   warps 4-11   decode K, eight keys a warp, handed over in four parts of 128
 //                dimensions; warps 12-19 decode V, 16 keys a warp, handed over
 //                in four parts of 32 keys
-//   warps 20-23  stage the queries of the next row
-//   warp 24      issues the MMAs (in the cluster's first block)
+//   warps 20-23  stage half of the queries of the next row (the V warps the
+//                other half)
+//   warp 24      issues the MMAs of S, warp 26 those of O (in the cluster's
+//                first block)
 //   warp 25      packs the pool rows of the list's entries into tiles
 //
-// K and V are single buffers that are never idle for long: the MMA order S(i
-// + 1), O(i) lets K be refilled during O and V during S.  The grid is
-// persistent: a cluster takes every n-th row, and the next row's queries,
-// keys and scores proceed while the last one's output is formed and stored.
+// K and V are single buffers that are never idle for long: S of a tile and O
+// of the one before run as their operands become ready, K is refilled during O
+// and V during S.  The grid is persistent: a cluster takes every n-th row, and
+// the next row's queries, keys and scores proceed while the last one's output
+// is formed and stored.  That boundary still costs some 14000 cycles a row, of
+// which staging the queries behind the row's last score takes 11000.
 //
 // Numbers as in dsa_attend.cu: latents exact in fp16, queries fp16 after an
-// exact power of two, P fp16 relative to a reference at most 2^8 below the
-// running maximum, scores, sums and outputs fp32.
+// exact power of two, P fp16 relative to a reference that the scores pass by
+// 2^8 at most, scores, sums and outputs fp32.
 #include <algorithm>
 
 #include "dsa_attend.cuh"
@@ -118,7 +123,7 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
 // Block scope is enough here and at every wait: the blocks share no data but
 // what the MMAs read, which the writer's proxy fence orders before its arrival.
 // (Release and acquire of cluster scope cost a fence over the block's global
-// loads each, 7500 cycles a tile instead of 3700.)
+// loads each, 1.96 ms instead of 1.60 when it was measured.)
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
