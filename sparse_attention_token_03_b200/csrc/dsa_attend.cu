@@ -18,11 +18,12 @@
 // blocks of [64 keys][128 bytes] with the 128-byte swizzle, read K-major for
 // S and M-major for O.
 //
-//   warps 0-3     softmax: S^T from TMEM, exp2, P^T to shared memory
+//   warps 0-3     softmax: S^T from TMEM, exp2, P^T to shared memory; at the
+//                 end of a row O^T from TMEM to the output
 //   warps 4-19    gather and decode: eight lanes per key load its 416 bytes one
 //                 tile ahead into registers, E2M1 -> fp16 times the block scale
-//                 (exact), and store the swizzled tile, two tile buffers; at
-//                 the end O^T from TMEM through shared memory to the output
+//                 (exact), and store the swizzled tile, two tile buffers; they
+//                 also stage the queries of the next row
 //   warps 20, 23  issue the MMAs of S, one for each tile buffer
 //   warp 22       issues the MMAs of O
 //   warp 21       reads the list and the block table and packs the pool rows of
@@ -36,12 +37,17 @@
 // group's two parts (dim_of gives the order; staged queries and output rows
 // follow it).
 //
+// The grid is persistent: a block takes every n-th row, and the next row's
+// lists, keys and scores proceed while the last one's output is formed and
+// stored (a block per row: 85 us where this takes 71, 501 rows of 16 heads and
+// 512 entries).
+//
 // What bounds it: with 64 heads the 128-byte wavefronts of shared memory, some
 // 3000 a tile (operands of the MMAs 1920, decoding 576, the rest P, slots and
-// conflicts) in 4200 cycles, the block's start and end included, against 1970
-// cycles of MMAs; with few heads the way round a tile buffer (decode, S,
-// softmax, O: some 5500 cycles for two tiles in flight).  999 rows of 64 heads
-// and 2048 entries: 535 us, 533 TFLOP/s; 148 rows of 16 heads: 64 us.
+// conflicts) in some 4100 cycles against 1970 cycles of MMAs; with few heads
+// the way round a tile buffer (decode, S, softmax, O: some 6000 cycles for two
+// tiles in flight).  999 rows of 64 heads and 2048 entries: 526 us, 541
+// TFLOP/s; 148 rows of 16 heads: 66 us.
 //
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
 // bits, 2^-10 .. 2688).  Queries go to fp16 too, each row scaled by the power
@@ -78,32 +84,34 @@ constexpr int kWorkThreads = (kSoftWarps + kLoadWarps) * 32;
 constexpr uint32_t kSoftRegs = 136, kLoadRegs = 72, kIssueRegs = 56;
 static_assert(kSoftRegs * 128 + kLoadRegs * 512 + kIssueRegs * 128 <= 80 * kAttThreads, "register pool");
 constexpr int kRing = 4;                         // tiles of slots that the list warp may be ahead
+// Tile word: keys, flags, and the number of the block's row modulo 256.
+constexpr int kLast = 1 << 16, kStop = 1 << 17, kRowShift = 20;
 constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr uint32_t kOutRow = 2 * kKvLat + 16;     // staged output row, padded against bank conflicts
-
 template <int NH>
 struct AttSmem {
-  static constexpr uint32_t q_block = NH * 128;
-  static constexpr uint32_t off_k = kBlocks * q_block;
+  static constexpr int q_bufs = NH <= 32 ? 2 : 1;        // rows of queries that fit next to the tile buffers
+  static constexpr uint32_t q_block = NH * 128, q_bytes = kBlocks * q_block;
+  static constexpr uint32_t off_k = (q_bufs * q_bytes + 1023) / 1024 * 1024;
   static constexpr uint32_t off_p = off_k + 2 * kTileBytes;
-  static constexpr uint32_t off_c = off_p + kKt * 128;   // per head: factor of a score in log2 units
-  static constexpr uint32_t off_f = off_c + NH * 4;      // per head: rescaling factor, then 1 / sum
-  static constexpr uint32_t off_ring = off_f + NH * 4;   // pool rows of the next tiles' keys
-  static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // keys of each ring tile, then of each buffer
+  static constexpr uint32_t off_c = off_p + kKt * 128;   // [2 rows] per head: factor of a score in log2 units
+  static constexpr uint32_t off_f = off_c + 2 * NH * 4;  // per head: rescaling factor, then 1 / sum
+  static constexpr uint32_t off_m = off_f + NH * 4;      // per head: reference, for the statistics
+  static constexpr uint32_t off_ring = off_m + NH * 4;   // pool rows of the next tiles' keys
+  static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // words of the ring tiles, then of the buffers
   static constexpr uint32_t off_bars = off_count + (kRing + 2) * 4;
-  // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], weights, output, drain [3]
-  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 4 + 5;
+  // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], queries full [2],
+  // queries free [2], factors free [2], weights, output, drain [3]
+  static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 10 + 5;
   static constexpr uint32_t off_misc = off_bars + 8 * n_bars;
   static constexpr uint32_t bytes = off_misc + 16;
-  static constexpr uint32_t request = bytes + 1024;      // slack to align the base to 1024
   static_assert(off_bars % 8 == 0, "mbarrier alignment");
-  static_assert(NH * kOutRow <= 2 * kTileBytes, "output staging");
 };
-static_assert(AttSmem<64>::request <= 227u * 1024u, "shared memory budget");
+static_assert(AttSmem<64>::bytes <= 227u * 1024u && AttSmem<32>::bytes <= 227u * 1024u, "shared memory budget");
 
 // One row, head block and list range of the grid.
 struct AttGrid {
   int head_blocks, splits, tiles;  // tiles: of a whole list
+  uint32_t items;                  // T * head_blocks * splits, below 2^31
   float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
   float2* part_ml;                 // [T][head_blocks][splits][NH]
   uint32_t* err;
@@ -148,26 +156,12 @@ __device__ __forceinline__ bool soft_bar_or(bool v) {
   return r != 0;
 }
 
-// Four 8 x 8 matrices of 16-bit fragments, transposed: lane 8 i + r gives the
-// address of column r of matrix i.
-__device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
-}
 // Four 8 x 8 matrices of 16-bit fragments: lane 8 i + r gives the address of
 // row r of matrix i.
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
-}
-// Bulk copy shared -> global (16-byte aligned, whole 16 bytes) and the wait until this thread's copies have read it.
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bulk_store_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // A key's raw bytes as one of its eight lanes (two groups of four) holds them:
 // 64 codes, their four scales and 8 rotary values.
@@ -198,28 +192,45 @@ __device__ __forceinline__ void load_raw(RawKey& r, const uint8_t* kv, int slot,
 __device__ __forceinline__ constexpr int part_of(int hi, int lo) { return hi + 2 * lo; }
 __device__ __forceinline__ constexpr int dim_of(int s, int p) { return 256 * (s & 1) + 64 * p + 32 * (s >> 1); }
 
-// Query rows to shared memory as the MMA reads them (see the file's comment),
-// row by row over the first kMmaWarp warps, the loads of all of a warp's rows
-// in flight.
+// Query rows r0, r0 + step, ... to shared memory as the MMA reads them (see the
+// file's comment), two rows in flight.
 template <int NH>
-__device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* smem, float* s_c,
-                                              int warp, int lane) {
-  constexpr int kRows = (NH + kMmaWarp - 1) / kMmaWarp;  // of a warp
-  uint4 v[kRows][3];
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    const int r = warp + k * kMmaWarp;
-    load_query_row(v[k], p, t, h0 + r, r < NH && h0 + r < p.H, lane);
-  }
+__device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* q_buf, float* s_c, int r0,
+                                              int step, int lane) {
+  auto live = [&](int r) { return r < NH && h0 + r < p.H; };
+  uint4 v[2][3];
+  load_query_row(v[0], p, t, h0 + r0, live(r0), lane);
+  load_query_row(v[1], p, t, h0 + r0 + step, live(r0 + step), lane);
 #pragma unroll 1
-  for (int r = warp; r < NH; r += kMmaWarp) {
-    store_query_row(v[0], p.scale, smem, AttSmem<NH>::q_block, r, s_c, lane, part_of);
+  for (int r = r0; r < NH; r += step) {
+    uint4 now[3];
 #pragma unroll
-    for (int k = 0; k + 1 < kRows; ++k) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) v[k][i] = v[k + 1][i];
+    for (int k = 0; k < 3; ++k) {
+      now[k] = v[0][k];
+      v[0][k] = v[1][k];
     }
+    load_query_row(v[1], p, t, h0 + r + 2 * step, live(r + 2 * step), lane);
+    store_query_row(now, p.scale, q_buf, AttSmem<NH>::q_block, r, s_c, lane, part_of);
   }
+}
+
+// A block's next item with a row to work on: item k and what it stands for.
+struct AttItem {
+  uint32_t k;
+  int64_t t;
+  int hb, split, seq;
+};
+__device__ __forceinline__ bool next_item(AttItem& it, const AttendParams& p, const AttGrid& g, bool report) {
+  for (; it.k < g.items; it.k += gridDim.x) {
+    const uint32_t row = it.k / static_cast<uint32_t>(g.splits);
+    it.split = static_cast<int>(it.k - row * g.splits);
+    it.t = row / static_cast<uint32_t>(g.head_blocks);
+    it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
+    it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
+    if (it.seq >= 0 && it.seq < p.B) return true;
+    if (it.seq >= p.B && report && p.status) atomicOr(p.status, kErrOverflow);  // else padding
+  }
+  return false;
 }
 
 // Float4 of a partial output block: 16 rows (dimensions) x NH columns (heads)
@@ -238,13 +249,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   // all of the tensor memory, so that it begins at column 0 (a constant for the
   // MMAs); shared memory keeps a second block off the SM anyway
   constexpr uint32_t kTmemCols = 512;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const uint32_t sQ = sbase, sK = sbase + L::off_k, sP = sbase + L::off_p;
+  const uint32_t sK = sbase + L::off_k, sP = sbase + L::off_p;
   float* s_c = reinterpret_cast<float*>(smem + L::off_c);
   float* s_f = reinterpret_cast<float*>(smem + L::off_f);
+  float* s_m = reinterpret_cast<float*>(smem + L::off_m);
   volatile int* s_ring = reinterpret_cast<volatile int*>(smem + L::off_ring);
   volatile int* s_ring_n = reinterpret_cast<volatile int*>(smem + L::off_count);
   volatile int* s_n = s_ring_n + kRing;
@@ -255,44 +265,38 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   auto bar_taken = [&](int r) { return bars + 8 * (4 * kParts + kRing + r); };
   auto bar_s = [&](int b) { return bars + 8 * (4 * kParts + 2 * kRing + b); };
   auto bar_read = [&](int b) { return bar_s(2 + b); };
-  const uint32_t bar_p = bar_s(4), bar_o = bar_p + 8, bar_drain = bar_p + 16;
+  auto bar_q = [&](int q) { return bar_s(4 + q); };
+  auto bar_q_free = [&](int q) { return bar_s(6 + q); };
+  auto bar_c_free = [&](int n) { return bar_s(8 + (n & 1)); };
+  const uint32_t bar_p = bar_s(10), bar_o = bar_p + 8, bar_drain = bar_p + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::off_misc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + L::off_misc + 8);
+  constexpr uint32_t tmem = 0;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t item = blockIdx.x;
-  const int split = static_cast<int>(item % g.splits);
-  const int hb = static_cast<int>(item / g.splits % g.head_blocks);
-  const int64_t t = item / g.splits / g.head_blocks;
-  const int h0 = hb * NH;
-  const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
-  if (seq < 0) return;  // padding
-  if (seq >= p.B) {
-    if (tid == 0 && p.status) atomicOr(p.status, kErrOverflow);
-    return;
-  }
-  const int j_lo = static_cast<int>(static_cast<int64_t>(g.tiles) * split / g.splits) * kKt;
-  const int j_hi = min(p.n, static_cast<int>(static_cast<int64_t>(g.tiles) * (split + 1) / g.splits) * kKt);
-  const int32_t* list = p.idx + t * p.n;
+  auto wait = [&](uint32_t bar, int parity) {
+    return __all_sync(~0u, wait_bar(bar, static_cast<uint32_t>(parity) & 1u, s_abort, g.err));
+  };
 
   if (tid == 0) {
     for (int i = 0; i < 2 * kParts; ++i) {
       mbar_init(bars + 8 * i, kLoadWarps / 2);
       mbar_init(bars + 8 * (2 * kParts + i), 1);
     }
-    mbar_init(bar_s(0), 1);
-    mbar_init(bar_s(1), 1);
-    mbar_init(bar_p, kSoftWarps);
-    mbar_init(bar_o, 1);
-    mbar_init(bar_read(0), kSoftWarps);
-    mbar_init(bar_read(1), kSoftWarps);
-    mbar_init(bar_drain, 1);
-    mbar_init(bar_drain + 8, 1);
-    mbar_init(bar_drain + 16, 1);
     for (int r = 0; r < kRing; ++r) {
       mbar_init(bar_listed(r), 1);
       mbar_init(bar_taken(r), kLoadWarps);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s(i), 1);
+      mbar_init(bar_read(i), kSoftWarps);
+      mbar_init(bar_q(i), kLoadWarps);
+      mbar_init(bar_q_free(i), kSoftWarps);
+      mbar_init(bar_c_free(i), kSoftWarps);
+    }
+    mbar_init(bar_p, kSoftWarps);
+    mbar_init(bar_o, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(bar_drain + 8 * i, 1);
     *s_abort = 0;
     fence_mbar_init();
   }
@@ -300,17 +304,21 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     tmem_alloc(smem_u32(s_tmem), kTmemCols);
     tmem_relinquish();
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
 
-  if (warp <= kMmaWarp) {
-    if (warp < kMmaWarp) {
-      stage_queries<NH>(p, t, h0, smem, s_c, warp, lane);
+  AttItem it{blockIdx.x, 0, 0, 0, 0};
+  // the first row's queries by all warps but the issuing ones and the list's
+  if (warp < kMmaWarp) {
+    AttItem first = it;
+    if (next_item(first, p, g, false)) {
+      stage_queries<NH>(p, first.t, first.hb * NH, smem, s_c, warp, kMmaWarp, lane);
       fence_proxy_async_smem();
     }
-    tc_fence_before();
-    named_bar_sync(2, kWorkThreads + 32);
-    tc_fence_after();
+    named_bar_sync(2, kWorkThreads);
   }
+
   // each warpgroup's share of the registers, set on its own path (behind a join
   // of the paths the compiler would hold all of them to the smallest)
   if (warp >= kMmaWarp) {
@@ -318,119 +326,133 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     if (warp == kListWarp) {
       // --------------------------------------------------------------- list
       // Packs the pool rows of the entries that name a key into tiles, ahead of
-      // the gathering warps; a tile of 0 keys ends the list.
-      const int32_t* table = p.block_table + static_cast<int64_t>(seq) * p.max_blocks;
+      // the gathering warps; a row without any gets one tile of no keys.
       int tile = 0, keys = 0;  // the open tile, and how many keys it has
       bool ok = true, bad = false;
-      auto publish = [&] {
-        if (lane == 0) s_ring_n[tile % kRing] = keys;
+      auto publish = [&](int flags) {  // the open tile
+        if (lane == 0) s_ring_n[tile % kRing] = keys | flags;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
       };
-      auto turn = [&] {  // publishes the open tile and opens the next one
-        publish();
+      auto turn = [&](int flags) {  // publishes the open tile and opens the next one
+        publish(flags);
         ++tile;
         keys = 0;
-        ok = __all_sync(~0u, wait_bar(bar_taken(tile % kRing), (static_cast<uint32_t>(tile / kRing) & 1u) ^ 1u, s_abort, g.err));
+        ok = wait(bar_taken(tile % kRing), tile / kRing + 1);
       };
-      int j0 = j_lo, pos[4];
+      int j0 = 0, j_hi = 0, pos[4];  // the item's entries that are left
+      const int32_t* list = nullptr;
       auto fetch = [&] {
 #pragma unroll
         for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
         j0 += 128;
       };
-      fetch();
-#pragma unroll 1
-      for (int left = (j_hi - j_lo + 127) >> 7; left > 0 && ok; --left) {  // steps of 128 entries
-        int slot[4];
-        slots_of(p, g.div, table, pos, slot, bad);
+      for (int n = 0; ok && next_item(it, p, g, lane == 0); it.k += gridDim.x, ++n) {
+        const int32_t* table = p.block_table + static_cast<int64_t>(it.seq) * p.max_blocks;
+        const int row = (n & 255) << kRowShift;
+        list = p.idx + it.t * p.n;
+        j0 = static_cast<int>(static_cast<int64_t>(g.tiles) * it.split / g.splits) * kKt;
+        j_hi = static_cast<int>(
+            min(static_cast<int64_t>(p.n), static_cast<int64_t>(g.tiles) * (it.split + 1) / g.splits * kKt));
+        const int steps = (j_hi - j0 + 127) >> 7;  // of 128 entries
         fetch();
 #pragma unroll 1
-        for (int k = 0; k < 4 && ok; ++k) {
-          const int mine = slot[0];
-          slot[0] = slot[1];
-          slot[1] = slot[2];
-          slot[2] = slot[3];
-          const uint32_t m = __ballot_sync(~0u, mine >= 0);
-          const int at = keys + __popc(m & lanemask_lt());
-          if (mine >= 0 && at < kKt) s_ring[tile % kRing * kKt + at] = mine;
-          keys += __popc(m);
-          if (keys >= kKt) {
-            const int rest = keys - kKt;
-            keys = kKt;
-            turn();
-            if (mine >= 0 && at >= kKt) s_ring[tile % kRing * kKt + at - kKt] = mine;
-            keys = rest;
+        for (int left = steps; left > 0 && ok; --left) {
+          int slot[4];
+          slots_of(p, g.div, table, pos, slot, bad);
+          fetch();
+#pragma unroll 1
+          for (int k = 0; k < 4 && ok; ++k) {
+            const int mine = slot[0];
+            slot[0] = slot[1];
+            slot[1] = slot[2];
+            slot[2] = slot[3];
+            const uint32_t m = __ballot_sync(~0u, mine >= 0);
+            const int at = keys + __popc(m & lanemask_lt());
+            if (mine >= 0 && at < kKt) s_ring[tile % kRing * kKt + at] = mine;
+            keys += __popc(m);
+            if (keys > kKt) {  // the rest starts the next tile, so this one is not the last
+              const int rest = keys - kKt;
+              keys = kKt;
+              turn(row);
+              if (mine >= 0 && at >= kKt) s_ring[tile % kRing * kKt + at - kKt] = mine;
+              keys = rest;
+            }
           }
         }
+        if (ok) turn(row | kLast);
       }
-      if (ok && keys > 0) turn();
-      if (ok) publish();
+      if (ok) publish(kStop);
       if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
     } else if (warp == kMmaWarp || warp == kMmaOddWarp) {
       // -------------------------------------------------- MMAs of the scores
       // One warp for each tile buffer: 36 MMAs take a warp longer to issue than
       // the tensor core to run when the heads are few.
-      constexpr uint32_t tmem = 0;
       constexpr uint32_t kIdS = idesc_att(64, NH, 0, 0, 0), kIdR = idesc_att(64, NH, 1, 0, 0);
-      const uint64_t dK = smem_desc_sw128(sK), dQ = smem_desc_sw128(sQ);
-      const uint32_t leader = elect_one();
+      const int b = warp == kMmaWarp ? 0 : 1;
+      const uint64_t dK = smem_desc_sw128(sK + b * kTileBytes);
+      const uint32_t leader = elect_one(), d = tmem + kTmemS + b * NH;
       bool ok = true;
-      const uint32_t drain = warp == kMmaWarp ? bar_drain : bar_drain + 16;
-      for (int i = warp == kMmaWarp ? 0 : 1; ok; i += 2) {
-        const int b = i & 1;
-        const uint32_t d = tmem + kTmemS + b * NH, ph = static_cast<uint32_t>(i >> 1) & 1u;
-        // lane by lane: the tile's four parts, and that the scores of tile i - 2 are read
-        const uint32_t mine = lane == 4 ? bar_read(b) : bar_full(b, lane & 3), par = lane == 4 ? ph ^ 1u : ph;
+      for (int k = 0; ok; ++k) {  // tile 2 k + b
+        // lane by lane: the tile's four parts, and that the scores of the buffer's last tile are read
+        const uint32_t mine = lane == 4 ? bar_read(b) : bar_full(b, lane & 3);
+        const uint32_t par = static_cast<uint32_t>(lane == 4 ? k + 1 : k) & 1u;
         uint32_t ready = 0;
-        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, g.err)) || s_n[b] == 0) break;
+        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, g.err))) break;
+        const int word = s_n[b];
+        if (word & kStop) break;
+        const int n = word >> kRowShift, q = L::q_bufs == 2 ? n & 1 : 0;
+        if (!(ok = wait(bar_q(q), L::q_bufs == 2 ? n >> 1 : n))) break;
         if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort, g.err))) break;
         tc_fence_after();
+        const uint64_t dQ = smem_desc_sw128(sbase + q * L::q_bytes);
 #pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
           if (!((ready >> s) & 1u)) {
             if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, g.err))) break;
             tc_fence_after();
           }
-          const uint64_t k0 = dK + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
+          const uint64_t k0 = dK + (2 * s * kBlockBytes >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_if<1>(leader, d, k0 + (((k >> 2) * kBlockBytes + 32 * (k & 3)) >> 4),
-                      q0 + (((k >> 2) * L::q_block + 32 * (k & 3)) >> 4), kIdS, s > 0 || k > 0);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_if<1>(leader, d, k0 + (((kk >> 2) * kBlockBytes + 32 * (kk & 3)) >> 4),
+                      q0 + (((kk >> 2) * L::q_block + 32 * (kk & 3)) >> 4), kIdS, s > 0 || kk > 0);
           if (s == 1) {  // each group brings half of the rotary block with its first part
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_if<1>(leader, d, dK + ((b * kTileBytes + 8 * kBlockBytes + 32 * k) >> 4),
-                        dQ + ((8 * L::q_block + 32 * k) >> 4), kIdR, 1);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_if<1>(leader, d, dK + ((8 * kBlockBytes + 32 * kk) >> 4), dQ + ((8 * L::q_block + 32 * kk) >> 4), kIdR, 1);
           }
           if (s == kParts - 1) commit_if(leader, bar_s(b));
         }
       }
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
+      const uint32_t drain = bar_drain + (b ? 16 : 0);
       commit_if(leader, drain);
       int unused = 0;
       wait_bar(drain, 0, &unused, g.err);
       __syncwarp();
     } else if (warp == kMmaOWarp) {
       // ------------------------------------------------- MMAs of the outputs
-      constexpr uint32_t tmem = 0;
       constexpr uint32_t kIdO = idesc_att(128, NH, 0, 1, 1);
       const uint64_t dV = desc_mn_sw128(sK, kBlockBytes), dP = desc_mn_sw128(sP, kBlockBytes);
       const uint32_t leader = elect_one();
-      for (int i = 0;; ++i) {  // O^T += V^T P^T of tile i
+      bool first = true;
+      for (int i = 0;; ++i) {  // O^T (+)= V^T P^T of tile i
         const int b = i & 1;
-        if (!__all_sync(~0u, wait_bar(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) || s_n[b] == 0) break;
-        if (!__all_sync(~0u, wait_bar(bar_p, static_cast<uint32_t>(i) & 1u, s_abort, g.err))) break;
+        if (!wait(bar_full(b, 0), i >> 1)) break;
+        const int word = s_n[b];
+        if ((word & kStop) || !wait(bar_p, i)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
           const uint64_t v = dV + ((b * kTileBytes + 2 * s * kBlockBytes) >> 4);
 #pragma unroll
           for (int k = 0; k < kKt / 16; ++k)
-            mma_if<1>(leader, tmem + kTmemO + s * NH, v + (k * 2048 >> 4), dP + (k * 2048 >> 4), kIdO, i > 0 || k > 0);
+            mma_if<1>(leader, tmem + kTmemO + s * NH, v + (k * 2048 >> 4), dP + (k * 2048 >> 4), kIdO, !first || k > 0);
           commit_if(leader, bar_empty(b, s));
         }
         commit_if(leader, bar_o);
+        first = word & kLast;
       }
       commit_if(leader, bar_drain + 8);
       int unused = 0;
@@ -439,35 +461,35 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     }
   } else if (warp >= kSoftWarps) {
     regs_dec<kLoadRegs>();
-    constexpr uint32_t tmem = 0;
     // ------------------------------------------------------------- gather
     const int lw = (warp - kSoftWarps) & 7, group = (warp - kSoftWarps) >> 3;
     const int key = lw * 8 + (lane & 7), part = lane >> 3;
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
-    RawKey raw;
-    int n_keys = 0, nt = -1;  // nt: tiles, once the end is known
     bool ok = true;
+    int n = 0;
+    if (next_item(it, p, g, false) && lane == 0) mbar_arrive(bar_q(0));  // staged above
+    RawKey raw;
+    int word = 0, stops = 0;
     for (int i = -1; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
       RawKey next;
-      int n_next = 0;
-      if (i < 0 || n_keys > 0) {
+      int next_word = kStop;
+      if (!(word & kStop)) {
         const int k = (i + 1) % kRing;
-        if (!__all_sync(~0u, wait_bar(bar_listed(k), static_cast<uint32_t>((i + 1) / kRing) & 1u, s_abort, g.err))) break;
-        n_next = s_ring_n[k];
-        load_raw(next, p.kv, s_ring[k * kKt + key], key < n_next, part, group);
+        if (!wait(bar_listed(k), (i + 1) / kRing)) break;
+        next_word = s_ring_n[k];
+        load_raw(next, p.kv, s_ring[k * kKt + key], key < (next_word & 0xFFFF), part, group);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_taken(k));
       }
       if (i >= 0) {
         const int b = i & 1;
-        const uint32_t ph = (static_cast<uint32_t>(i >> 1) & 1u) ^ 1u;
         const uint32_t tile = sK + b * kTileBytes + row;
 #pragma unroll 1
         for (int u = 0; u < kParts / 2; ++u) {
           const int s = 2 * u + group;
-          if (!(ok = __all_sync(~0u, wait_bar(bar_empty(b, s), ph, s_abort, g.err)))) break;
+          if (!(ok = wait(bar_empty(b, s), (i >> 1) + 1))) break;
           if (u == 0) {
-            if (warp == kSoftWarps && lane == 0) s_n[b] = n_keys;
+            if (warp == kSoftWarps && lane == 0) s_n[b] = word;
             sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
           }
           const __half2 sc =
@@ -485,98 +507,64 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_full(b, s));
-          if (n_keys == 0) break;  // the end of the list: part 0 alone carries it
+          if (word & kStop) break;  // part 0 alone carries it
         }
-        if (n_keys == 0) {  // told to both buffers' readers
-          if (nt >= 0) break;
-          nt = i;
+        if ((word & kStop) && ++stops == 2) break;  // told to both buffers' readers
+        if (ok && (word & kLast)) {  // the next row's queries
+          it.k += gridDim.x;
+          if (next_item(it, p, g, false)) {
+            ++n;
+            const int q = L::q_bufs == 2 ? n & 1 : 0;
+            ok = wait(bar_q_free(q), (L::q_bufs == 2 ? n >> 1 : n) + 1) && wait(bar_c_free(n), (n >> 1) + 1);
+            if (!ok) break;
+            stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps,
+                              lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_q(q));
+          }
         }
       }
       raw = next;
-      n_keys = n_next;
-    }
-    // ------------------------------------------------------------- output
-    // Warpgroup s takes part s: O^T from TMEM as 8 x 8 fragments with heads as
-    // columns, stored transposed to the tile buffers (nothing reads those any
-    // more), then one 1 KB bulk copy per head.
-    named_bar_sync(3, kWorkThreads);
-    tc_fence_after();
-    const int s = (warp - kSoftWarps) >> 2, pq = warp & 3;
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      uint32_t o[NH / 2];
-      if (nt > 0) {
-        tmem_ld_tile(tmem + kTmemO + s * NH + (static_cast<uint32_t>(pq * 32 + half * 16) << 16), o);
-        tmem_wait_ld();
-      } else {
-#pragma unroll
-        for (int k = 0; k < NH / 2; ++k) o[k] = 0u;
-      }
-      if (g.splits > 1) {
-#pragma unroll
-        for (int j = 0; j < NH / 8; ++j)
-          g.part_o[part_index<NH>(item, s, pq, half, j, lane)] =
-              make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
-                          __uint_as_float(o[4 * j + 3]));
-      } else {
-        const int dim = dim_of(s, pq) + 16 * half + (lane & 8);
-#pragma unroll
-        for (int j = 0; j < NH / 8; j += 2) {
-          uint32_t v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = *reinterpret_cast<const float2*>(s_f + 8 * (j + (k >> 1)) + 2 * (lane & 3));
-            const int x = 4 * j + 2 * k;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[x]) * f.x, __uint_as_float(o[x + 1]) * f.y);
-            v[k] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          stmatrix_t4(sK + (8 * (j + (lane >> 4)) + (lane & 7)) * kOutRow + 2 * dim, v);
-        }
-      }
-    }
-    tc_fence_before();
-    if (g.splits == 1) {
-      fence_proxy_async_smem();
-      named_bar_sync(4, kLoadWarps * 32);
-      const int h = tid - kSoftWarps * 32;
-      if (h < NH && h0 + h < p.H) {
-        bulk_store(p.out + (t * p.H + h0 + h) * kKvLat, sK + h * kOutRow, 2 * kKvLat);
-        bulk_store_wait();
-      }
+      word = next_word;
     }
   } else {
     regs_inc<kSoftRegs>();
-    constexpr uint32_t tmem = 0;
     // ------------------------------------------------------------ softmax
     // Threads hold pairs of columns (heads): pair j is columns 8 j + 2 (lane %
     // 4) and the next, at keys (rows) r0 and r0 + 8 of the warp's 16.
     constexpr int C = NH / 8;
-    float2 c[C], m[C], l[C];  // factor to log2 units, negated reference (from the first tile on), sum
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      c[j] = *reinterpret_cast<const float2*>(s_c + 8 * j + 2 * (lane & 3));
-      m[j] = make_float2(0.f, 0.f);
-      l[j] = make_float2(0.f, 0.f);
-    }
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const int r0 = lane >> 2;
     const uint32_t p0 = sP + (warp * 16 + (lane & 15)) * 128;  // this lane's row in the 8 x 8 stores
     float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH], while P is not in use
     bool ok = true;
-    for (int i = 0;; ++i) {
-      const int b = i & 1;
-      ok = __all_sync(~0u, wait_bar(bar_full(b, 0), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
-      const int n_keys = ok ? s_n[b] : 0;
-      if (n_keys > 0)
-        ok = __all_sync(~0u, wait_bar(bar_s(b), static_cast<uint32_t>(i >> 1) & 1u, s_abort, g.err)) && ok;
-      const bool end = !ok || n_keys == 0;
-      float x[NH / 2];
-      bool moved = false;
-      tc_fence_after();
+    int i = 0;
+    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x, ++n) {
+      float2 c[C], m[C], l[C];  // factor to log2 units, negated reference (from the first tile on), sum
+      for (bool first = true, last = false; !last; first = false, ++i) {
+        const int b = i & 1;
+        ok = wait(bar_s(b), i >> 1) && ok;
+        const int word = s_n[b], n_keys = word & 0xFFFF;
+        last = ok && (word & kLast);
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            c[j] = *reinterpret_cast<const float2*>(s_c + (n & 1) * NH + 8 * j + 2 * (lane & 3));
+            m[j] = make_float2(0.f, 0.f);
+            l[j] = make_float2(0.f, 0.f);
+          }
+        }
+        __syncwarp();
+        if (lane == 0 && first) mbar_arrive(bar_c_free(n));
+        if (lane == 0 && last) mbar_arrive(bar_q_free(L::q_bufs == 2 ? n & 1 : 0));  // all scores of the row are there
+        float x[NH / 2];
+        bool moved = false;
+        tc_fence_after();
 #pragma unroll 1
-      for (int pass = 0;; ++pass) {
-        float mx = -INFINITY;
-        if (!end) {  // x <- score - reference, -inf behind the last key; mx: the largest
+        for (int pass = 0;; ++pass) {
+          // x <- score - reference, -inf behind the last key; mx: the largest
+          float mx = -INFINITY;
           tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, reinterpret_cast<uint32_t(&)[NH / 2]>(x));
           tmem_wait_ld();
 #pragma unroll
@@ -596,109 +584,150 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           }
 #pragma unroll
           for (int k = 0; k < NH / 2; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
-        }
-        if (pass > 0) break;
-        // the same decision in all four warps; the first tile, the end of the
-        // list and a wait that gave up go this way too
-        moved = soft_bar_or(end || i == 0 || mx > kRise);
-        if (!moved) break;
-        if (i > 0) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
-        if (soft_bar_or(end || !ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-          float2 t = make_float2(fmaxf(x[4 * j], x[4 * j + 2]) - m[j].x, fmaxf(x[4 * j + 1], x[4 * j + 3]) - m[j].y);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            t.x = fmaxf(t.x, __shfl_xor_sync(~0u, t.x, o));
-            t.y = fmaxf(t.y, __shfl_xor_sync(~0u, t.y, o));
+          if (pass > 0) break;
+          // the same decision in all four warps; a row's first tile and a wait that gave up go this way too
+          moved = soft_bar_or(!ok || first || mx > kRise);
+          if (!moved) break;
+          if (!first) ok = wait(bar_o, i - 1) && ok;
+          if (soft_bar_or(!ok)) {
+            ok = false;
+            break;
           }
-          if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = t;
-        }
-        named_bar_sync(1, kSoftThreads);
+          tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          const int col = 8 * j + 2 * (lane & 3);
-          float2 n = i > 0 ? make_float2(-m[j].x, -m[j].y) : make_float2(-INFINITY, -INFINITY);
+          for (int j = 0; j < C; ++j) {
+            float2 t = make_float2(fmaxf(x[4 * j], x[4 * j + 2]) - m[j].x, fmaxf(x[4 * j + 1], x[4 * j + 3]) - m[j].y);
 #pragma unroll
-          for (int w = 0; w < kSoftWarps; ++w) {
-            const float2 e = *reinterpret_cast<const float2*>(exch + w * NH + col);
-            n.x = fmaxf(n.x, e.x);
-            n.y = fmaxf(n.y, e.y);
+            for (int o = 4; o < 32; o <<= 1) {
+              t.x = fmaxf(t.x, __shfl_xor_sync(~0u, t.x, o));
+              t.y = fmaxf(t.y, __shfl_xor_sync(~0u, t.y, o));
+            }
+            if (lane < 4) *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = t;
           }
-          const float2 f = i > 0 ? make_float2(ex2(-m[j].x - n.x), ex2(-m[j].y - n.y)) : make_float2(1.f, 1.f);
-          m[j] = make_float2(-n.x, -n.y);
-          l[j].x *= f.x;
-          l[j].y *= f.y;
-          if (warp == 0 && lane < 4) *reinterpret_cast<float2*>(s_f + col) = f;
-        }
-        named_bar_sync(1, kSoftThreads);
-        if (i > 0) {
+          named_bar_sync(1, kSoftThreads);
+#pragma unroll
+          for (int j = 0; j < C; ++j) {
+            const int col = 8 * j + 2 * (lane & 3);
+            float2 top = first ? make_float2(-INFINITY, -INFINITY) : make_float2(-m[j].x, -m[j].y);
+#pragma unroll
+            for (int w = 0; w < kSoftWarps; ++w) {
+              const float2 e = *reinterpret_cast<const float2*>(exch + w * NH + col);
+              top.x = fmaxf(top.x, e.x);
+              top.y = fmaxf(top.y, e.y);
+            }
+            if (top.x == -INFINITY) top.x = 0.f;  // no keys
+            if (top.y == -INFINITY) top.y = 0.f;
+            const float2 f = first ? make_float2(1.f, 1.f) : make_float2(ex2(-m[j].x - top.x), ex2(-m[j].y - top.y));
+            m[j] = make_float2(-top.x, -top.y);
+            l[j].x *= f.x;
+            l[j].y *= f.y;
+            if (warp == 0 && lane < 4) *reinterpret_cast<float2*>(s_f + col) = f;
+          }
+          named_bar_sync(1, kSoftThreads);
+          if (!first) {
 #pragma unroll 1
-          for (int q = 0; q < kParts * NH; q += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem + kTmemO + lane_base + q, o);
-            tmem_wait_ld();
+            for (int q = 0; q < kParts * NH; q += 16) {
+              uint32_t o[16];
+              tmem_ld16(tmem + kTmemO + lane_base + q, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s_f[q % NH + k]);
-            tmem_st16(tmem + kTmemO + lane_base + q, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s_f[q % NH + k]);
+              tmem_st16(tmem + kTmemO + lane_base + q, o);
+            }
+            tmem_wait_st();
           }
-          tmem_wait_st();
+        }
+        if (moved && !ok) break;  // decided by all four warps
+        uint32_t w[NH / 4];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const float2 a = make_float2(ex2(x[4 * j]), ex2(x[4 * j + 1])), d = make_float2(ex2(x[4 * j + 2]), ex2(x[4 * j + 3]));
+          l[j] = __fadd2_rn(l[j], __fadd2_rn(a, d));
+          const __half2 ha = __floats2half2_rn(a.x, a.y), hd = __floats2half2_rn(d.x, d.y);
+          w[2 * j] = *reinterpret_cast<const uint32_t*>(&ha);
+          w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hd);
+        }
+        // P of the last tile is consumed (checked above when the reference moved, at the end of the last row)
+        if (!moved) ok = wait(bar_o, i - 1) && ok;
+#pragma unroll
+        for (int j = 0; j < C; j += 2)
+          stmatrix4(p0 + (((j + (lane >> 4)) ^ (lane & 7)) << 4), w[2 * j], w[2 * j + 1], w[2 * j + 2], w[2 * j + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_p);
+          mbar_arrive(bar_read(b));
         }
       }
-      if (moved && !ok) break;  // decided by all four warps
-      uint32_t w[NH / 4];
+      // ----------------------------------------------------------- output
+      ok = ok && wait(bar_o, i - 1);
+      if (soft_bar_or(!ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        const float2 a = make_float2(ex2(x[4 * j]), ex2(x[4 * j + 1])), d = make_float2(ex2(x[4 * j + 2]), ex2(x[4 * j + 3]));
-        l[j] = __fadd2_rn(l[j], __fadd2_rn(a, d));
-        const __half2 ha = __floats2half2_rn(a.x, a.y), hd = __floats2half2_rn(d.x, d.y);
-        w[2 * j] = *reinterpret_cast<const uint32_t*>(&ha);
-        w[2 * j + 1] = *reinterpret_cast<const uint32_t*>(&hd);
-      }
-      // P of the last tile is consumed (checked above when the reference moved)
-      if (!moved) ok = __all_sync(~0u, wait_bar(bar_o, static_cast<uint32_t>(i - 1) & 1u, s_abort, g.err)) && ok;
 #pragma unroll
-      for (int j = 0; j < C; j += 2)
-        stmatrix4(p0 + (((j + (lane >> 4)) ^ (lane & 7)) << 4), w[2 * j], w[2 * j + 1], w[2 * j + 2], w[2 * j + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar_p);
-        mbar_arrive(bar_read(b));
+        for (int o = 4; o < 32; o <<= 1) {
+          l[j].x += __shfl_xor_sync(~0u, l[j].x, o);
+          l[j].y += __shfl_xor_sync(~0u, l[j].y, o);
+        }
+        if (lane < 4) {
+          *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = l[j];
+          if (warp == 0) *reinterpret_cast<float2*>(s_m + 8 * j + 2 * lane) = make_float2(-m[j].x, -m[j].y);
+        }
       }
-    }
-    // --------------------------------------------------------- statistics
-    // (the loop ended behind the last product: P is not in use)
-    named_bar_sync(1, kSoftThreads);
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l[j].x += __shfl_xor_sync(~0u, l[j].x, o);
-        l[j].y += __shfl_xor_sync(~0u, l[j].y, o);
+      named_bar_sync(1, kSoftThreads);
+      const int h0 = it.hb * NH;
+      if (tid < NH) {  // a head per thread
+        const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
+        if (g.splits > 1) {
+          g.part_ml[static_cast<int64_t>(it.k) * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_m[tid], sum);
+        } else {
+          s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
+          if (p.lse && h0 + tid < p.H)
+            p.lse[it.t * p.H + h0 + tid] = sum == 0.f ? -INFINITY : (s_m[tid] + log2f(sum)) * kLn2;
+        }
       }
-      if (lane < 4) {
-        *reinterpret_cast<float2*>(exch + warp * NH + 8 * j + 2 * lane) = l[j];
-        if (warp == 0) *reinterpret_cast<float2*>(s_c + 8 * j + 2 * lane) = make_float2(-m[j].x, -m[j].y);
-      }
-    }
-    named_bar_sync(1, kSoftThreads);
-    if (tid < NH) {  // a head per thread
-      const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
+      named_bar_sync(1, kSoftThreads);
       if (g.splits > 1) {
-        g.part_ml[item * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_c[tid], sum);
+#pragma unroll 1
+        for (int sh = 0; sh < 2 * kParts; ++sh) {  // part and half
+          uint32_t o[NH / 2];
+          tmem_ld_tile(tmem + kTmemO + (sh >> 1) * NH + lane_base + (static_cast<uint32_t>((sh & 1) * 16) << 16), o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < NH / 8; ++j)
+            g.part_o[part_index<NH>(it.k, sh >> 1, warp, sh & 1, j, lane)] =
+                make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
+                            __uint_as_float(o[4 * j + 3]));
+        }
       } else {
-        s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
-        if (p.lse && h0 + tid < p.H) p.lse[t * p.H + h0 + tid] = sum == 0.f ? -INFINITY : (s_c[tid] + log2f(sum)) * kLn2;
+#pragma unroll 1
+        for (int q = 0; q < kParts * NH; q += 16) {  // 16 heads of a part
+          const int s = q / NH, h = q % NH;
+          uint32_t o[16];
+          tmem_ld16(tmem + kTmemO + lane_base + q, o);
+          tmem_wait_ld();
+          const int dim = (dim_of(s, warp) + lane) & ~1;
+          uint16_t* dst = p.out + (it.t * p.H + h0 + h + (lane & 1)) * kKvLat + dim;
+          // lanes pair up: the even one stores two dimensions of a head, the odd one of the next head
+#pragma unroll
+          for (int k = 0; k < 16; k += 2) {
+            const float2 f = *reinterpret_cast<const float2*>(s_f + h + k);
+            const float a = __uint_as_float(o[k]) * f.x, d = __uint_as_float(o[k + 1]) * f.y;
+            const float other = __shfl_xor_sync(~0u, lane & 1 ? a : d, 1);
+            const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, d) : __floats2bfloat162_rn(a, other);
+            if (h0 + h + k + (lane & 1) < p.H) *reinterpret_cast<__nv_bfloat162*>(dst + k * kKvLat) = v;
+          }
+          __syncwarp();
+        }
       }
+      tc_fence_before();
+      named_bar_sync(1, kSoftThreads);  // s_f and P are free again
     }
-    tc_fence_before();
-    named_bar_sync(3, kWorkThreads);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -792,12 +821,11 @@ AttPlan plan_attend(int64_t T, int H, int n, int sms) {
 }
 
 template <int NH>
-cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, cudaStream_t st) {
-  constexpr int bytes = AttSmem<NH>::request;
+cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, int sms, cudaStream_t st) {
+  constexpr int bytes = AttSmem<NH>::bytes;
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const int64_t grid = p.T * g.head_blocks * g.splits;
-  attend_kv4_kernel<NH><<<static_cast<unsigned>(grid), kAttThreads, bytes, st>>>(p, g);
+  attend_kv4_kernel<NH><<<std::min(g.items, static_cast<uint32_t>(std::max(sms, 1))), kAttThreads, bytes, st>>>(p, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || g.splits == 1) return e;
   attend_join_kernel<NH><<<static_cast<unsigned>(p.T * g.head_blocks * kParts * (NH / 8)), 256, 0, st>>>(p, g);
@@ -814,9 +842,10 @@ cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, c
   if (p.H > 64) return launch_attend_kv4_pair(p, workspace, sms, st);
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttGrid g{P.head_blocks, P.splits, P.tiles, reinterpret_cast<float4*>(ws + P.off_o),
+  AttGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(p.T * P.head_blocks * P.splits),
+            reinterpret_cast<float4*>(ws + P.off_o),
             reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
-  return P.NH == 16 ? launch_nh<16>(p, g, st) : P.NH == 32 ? launch_nh<32>(p, g, st) : launch_nh<64>(p, g, st);
+  return P.NH == 16 ? launch_nh<16>(p, g, sms, st) : P.NH == 32 ? launch_nh<32>(p, g, sms, st) : launch_nh<64>(p, g, sms, st);
 }
 
 }  // namespace dsa
