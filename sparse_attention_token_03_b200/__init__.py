@@ -5,11 +5,17 @@ marshals arguments: it checks dtypes, shapes, devices and contiguity of torch
 tensors, allocates outputs and the workspace through torch, and passes raw
 pointers plus the current CUDA stream to the C ABI.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback.
+
+The serving calls, whose kernels take a few microseconds in a decode step, have
+a native host side (serve_binding.cpp, _serve_binding.so) that does the same
+for the common case in one call.
 """
 
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 from pathlib import Path
 
 import torch
@@ -44,6 +50,7 @@ class DSAError(RuntimeError):
 
 
 _lib = None
+_serve = None  # serve_binding.cpp
 
 
 def lib(build_if_missing: bool = True) -> ctypes.CDLL:
@@ -120,8 +127,30 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
         L.dsa_profile_enable.restype = I
         L.dsa_profile_read.argtypes = [P, P, I, P]
         L.dsa_profile_read.restype = I
+        _load_binding(L, build_if_missing)
         _lib = L
     return _lib
+
+
+def _load_binding(L: ctypes.CDLL, build_if_missing: bool):
+    global _serve
+    if build_if_missing and _build.binding_stale():
+        _build.build_binding()
+    loader = importlib.machinery.ExtensionFileLoader("_serve_binding", str(_build.BINDING))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve_binding", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.dsa_block_tables, L.dsa_index_prepare, L.dsa_index_prepare_fp8, L.dsa_kv4_write, L.dsa_kv4_read,
+        L.dsa_attend_kv4, L.dsa_attend_kv4_workspace_bytes)))
+    _serve = module
+
+
+def _native():
+    """serve_binding.cpp: the common case of the serving calls.  It returns None
+    where an argument is anything else, and the caller goes on to its own checks."""
+    if _serve is None:
+        lib()
+    return _serve
 
 
 def _check(rc: int):
@@ -602,10 +631,18 @@ def dsa_block_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_tabl
     entries of newly needed blocks are filled in place from free_pages
     (n_free,) int32, starting at free_begin (1,) int32; T_cap rows.  Returns
     (slot_map, position, row_seq, row_start, seq_len, free_end), all int32:
-    (T_cap,) three times, -1 past the last token, then (B + 1,), (B,), (1,).
+    (T_cap,) three times, -1 past the last token, then (B + 1,), (B,), (1,);
+    without tensors for them they are parts of one allocation.
     When a length is out of range or rows or pages do not suffice, no request
     gets new tokens and status bit 1 is set.
     """
+    if slot_map is position is row_seq is row_start is seq_len is free_end is None:
+        r = _native().block_tables(cached_len, new_len, block_table, free_pages, free_begin, n_pages, page_size, T_cap,
+                                   status)
+        if type(r) is tuple:
+            return r
+        if r is not None:
+            _check(r)
     dev = block_table.device
     _need(cached_len, "cached_len", torch.int32, 1, dev)
     B = cached_len.shape[0]
@@ -619,18 +656,12 @@ def dsa_block_tables(cached_len: torch.Tensor, new_len: torch.Tensor, block_tabl
     new = _arg(new_len, "new_len", torch.int32, (B,), dev)
     begin = _arg(free_begin, "free_begin", torch.int32, (1,), dev)
     _need(free_pages, "free_pages", torch.int32, 1, dev)
-    if slot_map is None and position is None and row_seq is None and row_start is None and seq_len is None \
-            and free_end is None:
-        # one allocation for the six
-        slot_map, position, row_seq, row_start, seq_len, free_end = block_table.new_empty(
-            3 * T_cap + 2 * B + 2).split_with_sizes([T_cap, T_cap, T_cap, B + 1, B, 1])
-    else:
-        slot_map = _out(slot_map, "slot_map", torch.int32, (T_cap,), dev)
-        position = _out(position, "position", torch.int32, (T_cap,), dev)
-        row_seq = _out(row_seq, "row_seq", torch.int32, (T_cap,), dev)
-        row_start = _out(row_start, "row_start", torch.int32, (B + 1,), dev)
-        seq_len = _out(seq_len, "seq_len", torch.int32, (B,), dev)
-        free_end = _out(free_end, "free_end", torch.int32, (1,), dev)
+    slot_map = _out(slot_map, "slot_map", torch.int32, (T_cap,), dev)
+    position = _out(position, "position", torch.int32, (T_cap,), dev)
+    row_seq = _out(row_seq, "row_seq", torch.int32, (T_cap,), dev)
+    row_start = _out(row_start, "row_start", torch.int32, (B + 1,), dev)
+    seq_len = _out(seq_len, "seq_len", torch.int32, (B,), dev)
+    free_end = _out(free_end, "free_end", torch.int32, (1,), dev)
     _call(lib().dsa_block_tables, dev, cached_len.data_ptr(), new, B, block_table.data_ptr(), max_blocks, free_pages.data_ptr(),
           free_pages.shape[0], begin, int(n_pages), int(page_size), T_cap, slot_map.data_ptr(), position.data_ptr(),
           row_seq.data_ptr(), row_start.data_ptr(), seq_len.data_ptr(), free_end.data_ptr(),
@@ -672,6 +703,14 @@ def dsa_index_prepare(q: torch.Tensor, k: torch.Tensor, position: torch.Tensor, 
     Rows with position < 0 are padding and left as they were.  Returns
     (q_out (T, H, 128) bf16, k_out); q_out may be q.
     """
+    if q_out is None and isinstance(q, torch.Tensor):
+        q_out = torch.empty_like(q)
+    r = _native().prepare(0, q, k, position, inv_freq, k_out, None, slot_map, NORMS.get(q_norm), q_weight, q_bias,
+                          NORMS.get(k_norm), k_weight, k_bias, float(eps), bool(interleaved), q_out, None, status)
+    if r == 0:
+        return q_out, k_out
+    if r is not None:
+        _check(r)
     dev, T, H, d, head, slots, st = _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight,
                                                   q_bias, k_norm, k_weight, k_bias, status)
     kp = _arg(k_out, "k_out", torch.bfloat16, k_out.shape, dev)
@@ -688,6 +727,17 @@ def dsa_index_prepare_fp8(q: torch.Tensor, k: torch.Tensor, position: torch.Tens
     the inputs of dsa_index_prefill_fp8.  Returns (q_out (T, H, 128), q_scale
     (T, H), k_out (..., 128), k_scale_out (...,)); codes are uint8 or
     float8_e4m3fn tensors."""
+    if isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.uint8, device=q.device)
+        if q_scale_out is None:
+            q_scale_out = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    r = _native().prepare(1, q, k, position, inv_freq, k_out, k_scale_out, slot_map, NORMS.get(q_norm), q_weight, q_bias,
+                          NORMS.get(k_norm), k_weight, k_bias, float(eps), bool(interleaved), q_out, q_scale_out, status)
+    if r == 0:
+        return q_out, q_scale_out, k_out, k_scale_out
+    if r is not None:
+        _check(r)
     dev, T, H, d, head, slots, st = _prepare_args(q, k, position, inv_freq, k_out, slot_map, q_norm, q_weight,
                                                   q_bias, k_norm, k_weight, k_bias, status)
     kc = _codes(k_out, "k_out", k_out.dim(), dev)
@@ -717,6 +767,11 @@ def dsa_kv4_write(latent: torch.Tensor, rope: torch.Tensor, kv_pages: torch.Tens
     (int32; < 0: padding) of the page pool kv_pages (n_pages, page_size, 416)
     uint8.  Returns kv_pages.
     """
+    r = _native().kv4_write(latent, rope, kv_pages, slot_map, status)
+    if r == 0:
+        return kv_pages
+    if r is not None:
+        _check(r)
     n_slots = _kv4_pool(kv_pages)
     dev = kv_pages.device
     _need(slot_map, "slot_map", torch.int32, 1, dev)
@@ -731,6 +786,11 @@ def dsa_kv4_read(kv_pages: torch.Tensor, slot_map: torch.Tensor, latent_out=None
     """Rows slot_map (T,) int32 of the 4-bit latent cache in bf16 (exact):
     (latent (T, 512), rope (T, 64)).  Rows with a slot < 0 are left as they
     were."""
+    r = _native().kv4_read(kv_pages, slot_map, latent_out, rope_out, status)
+    if r == 0:
+        return latent_out, rope_out
+    if r is not None:
+        _check(r)
     n_slots = _kv4_pool(kv_pages)
     dev = kv_pages.device
     _need(slot_map, "slot_map", torch.int32, 1, dev)
@@ -758,6 +818,11 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
     row's sequence (< 0: padding, left as it was); without it row t reads
     sequence t.  Returns (out (T, H, 512) bf16, lse (T, H) fp32).
     """
+    r = _native().attend(q, kv_pages, block_table, idx, float(scale), row_seq, out, lse, workspace, status)
+    if type(r) is tuple:
+        return r
+    if r is not None:
+        _check(r)
     _kv4_pool(kv_pages)
     dev = kv_pages.device
     _need(q, "q", torch.bfloat16, 3, dev)

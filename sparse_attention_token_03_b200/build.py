@@ -1,4 +1,5 @@
-"""Build libdsa_index.so in-tree with nvcc for sm_100a (no torch JIT cache)."""
+"""Build libdsa_index.so in-tree with nvcc for sm_100a (no torch JIT cache), and
+_serve_binding.so, the native host side of the serving calls, with g++."""
 
 from __future__ import annotations
 
@@ -12,6 +13,8 @@ PKG = Path(__file__).resolve().parent
 CSRC = PKG / "csrc"
 INCLUDE = PKG.parent / "include"
 LIB = PKG / "libdsa_index.so"
+BINDING_SRC = PKG / "serve_binding.cpp"
+BINDING = PKG / "_serve_binding.so"
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -57,5 +60,35 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     return LIB
 
 
+def binding_stale() -> bool:
+    if not BINDING.exists():
+        return True
+    t = BINDING.stat().st_mtime
+    return any(p.stat().st_mtime > t for p in (BINDING_SRC, *INCLUDE.glob("*.h")))
+
+
+def build_binding(force: bool = False) -> Path:
+    """Compile serve_binding.cpp against the installed torch and Python."""
+    if not force and not binding_stale():
+        return BINDING
+    import sysconfig
+
+    import torch
+
+    tdir = Path(torch.__file__).parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    tmp = BINDING.with_suffix(f".{os.getpid()}.tmp")
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+        f"-I{tdir}/include", f"-I{tdir}/include/torch/csrc/api/include", f"-I{sysconfig.get_path('include')}",
+        f"-I{cuda}/include", "-o", str(tmp), str(BINDING_SRC), f"-L{tdir}/lib",
+        "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10_cuda", "-lc10",
+    ])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
