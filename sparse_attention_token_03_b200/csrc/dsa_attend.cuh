@@ -217,38 +217,60 @@ __device__ __forceinline__ void load_query_row(uint4 (&v)[3], const AttendParams
 // of quarter p of it are the latent dimensions 256 hi + 64 p + 32 lo .. + 31
 // with s = part_of(hi, lo); block 8 holds the rotary ones.  Few instructions
 // rather than fast ones: this runs once a row, from a cold instruction cache.
-template <typename PartOf>
-__device__ __forceinline__ void store_query_row(const uint4 (&v)[3], float scale, uint8_t* smem, uint32_t q_block, int r,
-                                                float* s_c, int lane, PartOf part_of) {
-  uint32_t m = 0;  // largest magnitude as bf16 bits (two lanes of 16)
+// R rows at once, since one row is a chain of dependent instructions.
+template <int R, typename PartOf>
+__device__ __forceinline__ void store_query_rows(const uint4 (&v)[R][3], float scale, uint8_t* smem, uint32_t q_block,
+                                                 const int (&r)[R], float* s_c, int lane, PartOf part_of) {
+  uint32_t m[R];  // largest magnitude as bf16 bits (two lanes of 16)
+  float up[R];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    m = __vmaxu2(m, __vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu));
-    m = __vmaxu2(m, __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+  for (int w = 0; w < R; ++w) {
+    m[w] = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      m[w] = __vmaxu2(m[w], __vmaxu2(v[w][i].x & 0x7FFF7FFFu, v[w][i].y & 0x7FFF7FFFu));
+      m[w] = __vmaxu2(m[w], __vmaxu2(v[w][i].z & 0x7FFF7FFFu, v[w][i].w & 0x7FFF7FFFu));
+    }
   }
-  m = __reduce_max_sync(~0u, max(m & 0xFFFFu, m >> 16));
-  const int e = min(141 - static_cast<int>(m >> 7), 126);  // biased exponent field -> shift
-  const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-  if (lane == 0) s_c[r] = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  uint4 now = v[0], next = v[1], last = v[2];
+#pragma unroll
+  for (int w = 0; w < R; ++w) {
+    m[w] = __reduce_max_sync(~0u, max(m[w] & 0xFFFFu, m[w] >> 16));
+    const int e = min(141 - static_cast<int>(m[w] >> 7), 126);  // biased exponent field -> shift
+    up[w] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    if (lane == 0) s_c[r[w]] = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  }
+  uint4 now[R], next[R], last[R];
+#pragma unroll
+  for (int w = 0; w < R; ++w) now[w] = v[w][0], next[w] = v[w][1], last[w] = v[w][2];
 #pragma unroll 1
   for (int c = lane; c < kQChunks; c += 32) {
     const bool rotary = c >= kKvLat / 8;
-    uint32_t u[4] = {now.x, now.y, now.z, now.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float a = __uint_as_float(u[k] << 16) * up, b = __uint_as_float(u[k] & 0xFFFF0000u) * up;
-      const __half2 h = __floats2half2_rn(a, b);
-      const __nv_bfloat162 f = __floats2bfloat162_rn(a, b);
-      u[k] = rotary ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
-    }
     const int p = (c >> 3) & 3;
     const int blk = rotary ? 8 : 2 * part_of(c >> 5, (c >> 2) & 1) + (p >> 1);
     const int at = rotary ? c & 7 : 4 * (p & 1) + (c & 3);
-    *reinterpret_cast<uint4*>(smem + blk * q_block + r * 128 + ((at ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
-    now = next;
-    next = last;
+#pragma unroll
+    for (int w = 0; w < R; ++w) {
+      uint32_t u[4] = {now[w].x, now[w].y, now[w].z, now[w].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float a = __uint_as_float(u[k] << 16) * up[w], b = __uint_as_float(u[k] & 0xFFFF0000u) * up[w];
+        const __half2 h = __floats2half2_rn(a, b);
+        const __nv_bfloat162 f = __floats2bfloat162_rn(a, b);
+        u[k] = rotary ? *reinterpret_cast<const uint32_t*>(&f) : *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(smem + blk * q_block + r[w] * 128 + ((at ^ (r[w] & 7)) << 4)) =
+          make_uint4(u[0], u[1], u[2], u[3]);
+      now[w] = next[w];
+      next[w] = last[w];
+    }
   }
+}
+template <typename PartOf>
+__device__ __forceinline__ void store_query_row(const uint4 (&v)[3], float scale, uint8_t* smem, uint32_t q_block, int r,
+                                                float* s_c, int lane, PartOf part_of) {
+  const uint4 one[1][3] = {{v[0], v[1], v[2]}};
+  const int rows[1] = {r};
+  store_query_rows<1>(one, scale, smem, q_block, rows, s_c, lane, part_of);
 }
 
 }  // namespace dsa

@@ -256,20 +256,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       const char* src = reinterpret_cast<const char*>(p.q + (item.t * p.H + h0 + r0) * kKvQ);
       for (int b = lane * 128; b < min(rows, p.H - h0 - r0) * 2 * kKvQ; b += 32 * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(src + b));
+      auto live = [&](int r) { return h0 + r < p.H; };
       uint4 v[2][3];
-      load_query_row(v[0], p, item.t, h0 + r0, h0 + r0 < p.H, lane);
-      load_query_row(v[1], p, item.t, h0 + r0 + 1, h0 + r0 + 1 < p.H, lane);
+      load_query_row(v[0], p, item.t, h0 + r0, live(r0), lane);
+      load_query_row(v[1], p, item.t, h0 + r0 + 1, live(r0 + 1), lane);
       if (!wait(kBarQE, n + 1) || !wait(kBarCE, n + 1)) return false;
 #pragma unroll 1
-      for (int r = r0; r < r0 + rows; ++r) {
-        uint4 now[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          now[k] = v[0][k];
-          v[0][k] = v[1][k];
-        }
-        load_query_row(v[1], p, item.t, h0 + r + 2, r + 2 < r0 + rows && h0 + r + 2 < p.H, lane);
-        store_query_row(now, p.scale, smem + kOffQ, kBlk, r, s_c, lane, part_of);
+      for (int r = r0;;) {
+        const int two[2] = {r, r + 1};
+        store_query_rows<2>(v, p.scale, smem + kOffQ, kBlk, two, s_c, lane, part_of);
+        r += 2;
+        if (r >= r0 + rows) break;
+        load_query_row(v[0], p, item.t, h0 + r, live(r), lane);
+        load_query_row(v[1], p, item.t, h0 + r + 1, live(r + 1), lane);
       }
       fence_proxy_async_smem();
     }
