@@ -214,6 +214,21 @@ __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, 
   }
 }
 
+// The same rows for a whole number of pairs, two at once.
+template <int NH>
+__device__ __forceinline__ void stage_query_pairs(const AttendParams& p, int64_t t, int h0, uint8_t* q_buf, float* s_c,
+                                                  int r0, int step, int lane) {
+  auto live = [&](int r) { return h0 + r < p.H; };
+#pragma unroll 1
+  for (int r = r0; r < NH; r += 2 * step) {
+    uint4 v[2][3];
+    load_query_row(v[0], p, t, h0 + r, live(r), lane);
+    load_query_row(v[1], p, t, h0 + r + step, live(r + step), lane);
+    const int two[2] = {r, r + step};
+    store_query_rows<2>(v, p.scale, q_buf, AttSmem<NH>::q_block, two, s_c, lane, part_of);
+  }
+}
+
 // A block's next item with a row to work on: item k and what it stands for.
 struct AttItem {
   uint32_t k;
@@ -515,10 +530,19 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           if (next_item(it, p, g, false)) {
             ++n;
             const int q = L::q_bufs == 2 ? n & 1 : 0;
+            // on their way to L2 during the wait
+            const char* src = reinterpret_cast<const char*>(p.q + (it.t * p.H + it.hb * NH) * kKvQ);
+            const int bytes = min(NH, p.H - it.hb * NH) * 2 * kKvQ;
+            for (int at = (tid - kSoftThreads) * 128; at < bytes; at += kLoadWarps * 32 * 128)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
             ok = wait(bar_q_free(q), (L::q_bufs == 2 ? n >> 1 : n) + 1) && wait(bar_c_free(n), (n >> 1) + 1);
             if (!ok) break;
-            stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps,
-                              lane);
+            if constexpr (NH >= 2 * kLoadWarps)
+              stage_query_pairs<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
+                                    kLoadWarps, lane);
+            else
+              stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
+                                kLoadWarps, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_q(q));
