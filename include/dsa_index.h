@@ -517,6 +517,8 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  *   lse          device, [T][H] fp32 (natural logarithm), or NULL
  *   workspace    device, 256-byte aligned, of
  *                dsa_attend_kv4_workspace_bytes(T, H, n) bytes
+ *                (of the current device); calls that may run at the same time
+ *                need workspaces of their own
  * Scores, softmax statistics and output sums are fp32.  Results do not depend
  * on the rest of the batch's contents.  T == 0 is a no-op.  Requires
  * max_blocks * page_size < 2^31, n_pages * page_size < 2^31, T * H < 2^31.

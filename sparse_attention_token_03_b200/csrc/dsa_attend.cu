@@ -37,16 +37,16 @@
 // group's two parts (dim_of gives the order; staged queries and output rows
 // follow it).
 //
-// The grid is persistent: a block takes every n-th row, and the next row's
-// lists, keys and scores proceed while the last one's output is formed and
-// stored (a block per row: 85 us where this takes 71, 501 rows of 16 heads and
-// 512 entries).
+// The grid is persistent: a block takes rows as it gets free, and the next
+// row's lists, queries, keys and scores proceed while the last one's output is
+// formed and stored (a block per row: 85 us where this takes 70, 501 rows of 16
+// heads and 512 entries).
 //
 // What bounds it: with 64 heads the 128-byte wavefronts of shared memory, some
 // 3000 a tile (operands of the MMAs 1920, decoding 576, the rest P, slots and
 // conflicts) in some 4100 cycles against 1970 cycles of MMAs; with few heads
 // the way round a tile buffer (decode, S, softmax, O: some 6000 cycles for two
-// tiles in flight).  999 rows of 64 heads and 2048 entries: 526 us, 541
+// tiles in flight).  999 rows of 64 heads and 2048 entries: 506 us, 563
 // TFLOP/s; 148 rows of 16 heads: 66 us.
 //
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
@@ -98,7 +98,7 @@ struct AttSmem {
   static constexpr uint32_t off_m = off_f + NH * 4;      // per head: reference, for the statistics
   static constexpr uint32_t off_ring = off_m + NH * 4;   // pool rows of the next tiles' keys
   static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // words of the ring tiles, then of the buffers
-  static constexpr uint32_t off_bars = off_count + (kRing + 2) * 4;
+  static constexpr uint32_t off_bars = off_count + 2 * (kRing + 2) * 4;  // and their items
   // part full and empty [2 buffers][4], ring full and empty, scores [2], scores read [2], queries full [2],
   // queries free [2], factors free [2], weights, output, drain [3]
   static constexpr uint32_t n_bars = 4 * kParts + 2 * kRing + 10 + 5;
@@ -112,6 +112,8 @@ static_assert(AttSmem<64>::bytes <= 227u * 1024u && AttSmem<32>::bytes <= 227u *
 struct AttGrid {
   int head_blocks, splits, tiles;  // tiles: of a whole list
   uint32_t items;                  // T * head_blocks * splits, below 2^31
+  uint32_t* next;                  // null (block b takes items b, b + grid, ...) or a counter at 0 of the items behind
+                                   // the blocks' first ones that are taken
   float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
   float2* part_ml;                 // [T][head_blocks][splits][NH]
   uint32_t* err;
@@ -229,23 +231,18 @@ __device__ __forceinline__ void stage_query_pairs(const AttendParams& p, int64_t
   }
 }
 
-// A block's next item with a row to work on: item k and what it stands for.
+// What item k stands for; false for padding and a sequence that does not exist.
 struct AttItem {
-  uint32_t k;
   int64_t t;
   int hb, split, seq;
 };
-__device__ __forceinline__ bool next_item(AttItem& it, const AttendParams& p, const AttGrid& g, bool report) {
-  for (; it.k < g.items; it.k += gridDim.x) {
-    const uint32_t row = it.k / static_cast<uint32_t>(g.splits);
-    it.split = static_cast<int>(it.k - row * g.splits);
-    it.t = row / static_cast<uint32_t>(g.head_blocks);
-    it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
-    it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
-    if (it.seq >= 0 && it.seq < p.B) return true;
-    if (it.seq >= p.B && report && p.status) atomicOr(p.status, kErrOverflow);  // else padding
-  }
-  return false;
+__device__ __forceinline__ bool item_of(AttItem& it, uint32_t k, const AttendParams& p, const AttGrid& g) {
+  const uint32_t row = k / static_cast<uint32_t>(g.splits);
+  it.split = static_cast<int>(k - row * g.splits);
+  it.t = row / static_cast<uint32_t>(g.head_blocks);
+  it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
+  it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
+  return it.seq >= 0 && it.seq < p.B;
 }
 
 // Float4 of a partial output block: 16 rows (dimensions) x NH columns (heads)
@@ -273,6 +270,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   volatile int* s_ring = reinterpret_cast<volatile int*>(smem + L::off_ring);
   volatile int* s_ring_n = reinterpret_cast<volatile int*>(smem + L::off_count);
   volatile int* s_n = s_ring_n + kRing;
+  volatile int *s_ring_k = s_n + 2, *s_k = s_ring_k + kRing;
   const uint32_t bars = sbase + L::off_bars;
   auto bar_full = [&](int b, int s) { return bars + 8 * (b * kParts + s); };
   auto bar_empty = [&](int b, int s) { return bars + 8 * (2 * kParts + b * kParts + s); };
@@ -323,12 +321,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   __syncthreads();
   tc_fence_after();
 
-  AttItem it{blockIdx.x, 0, 0, 0, 0};
-  // the first row's queries by all warps but the issuing ones and the list's
+  AttItem it;
+  const bool first_ok = item_of(it, blockIdx.x, p, g);
+  // the queries of the block's first item by all warps but the issuing ones and the list's
   if (warp < kMmaWarp) {
-    AttItem first = it;
-    if (next_item(first, p, g, false)) {
-      stage_queries<NH>(p, first.t, first.hb * NH, smem, s_c, warp, kMmaWarp, lane);
+    if (first_ok) {
+      stage_queries<NH>(p, it.t, it.hb * NH, smem, s_c, warp, kMmaWarp, lane);
       fence_proxy_async_smem();
     }
     named_bar_sync(2, kWorkThreads);
@@ -344,8 +342,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       // the gathering warps; a row without any gets one tile of no keys.
       int tile = 0, keys = 0;  // the open tile, and how many keys it has
       bool ok = true, bad = false;
+      uint32_t k = blockIdx.x;
       auto publish = [&](int flags) {  // the open tile
-        if (lane == 0) s_ring_n[tile % kRing] = keys | flags;
+        if (lane == 0) {
+          s_ring_n[tile % kRing] = keys | flags;
+          s_ring_k[tile % kRing] = static_cast<int>(k);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_listed(tile % kRing));
       };
@@ -362,7 +364,19 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         for (int k = 0; k < 4; ++k) pos[k] = j0 + 32 * k + lane < j_hi ? __ldg(list + j0 + 32 * k + lane) : -1;
         j0 += 128;
       };
-      for (int n = 0; ok && next_item(it, p, g, lane == 0); it.k += gridDim.x, ++n) {
+      auto advance = [&] {
+        if (g.next) {
+          if (lane == 0) k = gridDim.x + atomicAdd(g.next, 1u);
+          k = __shfl_sync(~0u, k, 0);
+        } else {
+          k += gridDim.x;
+        }
+      };
+      for (int n = 0; ok && k < g.items; advance()) {
+        if (!item_of(it, k, p, g)) {
+          bad |= it.seq >= p.B;  // else padding
+          continue;
+        }
         const int32_t* table = p.block_table + static_cast<int64_t>(it.seq) * p.max_blocks;
         const int row = (n & 255) << kRowShift;
         list = p.idx + it.t * p.n;
@@ -377,7 +391,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           slots_of(p, g.div, table, pos, slot, bad);
           fetch();
 #pragma unroll 1
-          for (int k = 0; k < 4 && ok; ++k) {
+          for (int q = 0; q < 4 && ok; ++q) {
             const int mine = slot[0];
             slot[0] = slot[1];
             slot[1] = slot[2];
@@ -396,6 +410,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           }
         }
         if (ok) turn(row | kLast);
+        ++n;
       }
       if (ok) publish(kStop);
       if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
@@ -481,17 +496,21 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     const int key = lw * 8 + (lane & 7), part = lane >> 3;
     const uint32_t row = static_cast<uint32_t>(key) * 128, sw = static_cast<uint32_t>(key & 7);
     bool ok = true;
-    int n = 0;
-    if (next_item(it, p, g, false) && lane == 0) mbar_arrive(bar_q(0));  // staged above
+    int n = -1;  // rows staged, less one
+    if (first_ok) {
+      n = 0;
+      if (lane == 0) mbar_arrive(bar_q(0));
+    }
     RawKey raw;
-    int word = 0, stops = 0;
+    int word = 0, item = 0, stops = 0;
     for (int i = -1; ok; ++i) {  // loads of tile i + 1, then tile i to shared memory
       RawKey next;
-      int next_word = kStop;
+      int next_word = kStop, next_item = 0;
       if (!(word & kStop)) {
         const int k = (i + 1) % kRing;
         if (!wait(bar_listed(k), (i + 1) / kRing)) break;
         next_word = s_ring_n[k];
+        next_item = s_ring_k[k];
         load_raw(next, p.kv, s_ring[k * kKt + key], key < (next_word & 0xFFFF), part, group);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_taken(k));
@@ -504,7 +523,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           const int s = 2 * u + group;
           if (!(ok = wait(bar_empty(b, s), (i >> 1) + 1))) break;
           if (u == 0) {
-            if (warp == kSoftWarps && lane == 0) s_n[b] = word;
+            if (warp == kSoftWarps && lane == 0) {
+              s_n[b] = word;
+              s_k[b] = item;
+            }
             sts128(tile + 8 * kBlockBytes + (((2 * part + group) ^ sw) << 4), raw.rope.x, raw.rope.y, raw.rope.z, raw.rope.w);
           }
           const __half2 sc =
@@ -525,30 +547,30 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           if (word & kStop) break;  // part 0 alone carries it
         }
         if ((word & kStop) && ++stops == 2) break;  // told to both buffers' readers
-        if (ok && (word & kLast)) {  // the next row's queries
-          it.k += gridDim.x;
-          if (next_item(it, p, g, false)) {
-            ++n;
-            const int q = L::q_bufs == 2 ? n & 1 : 0;
-            // on their way to L2 during the wait
-            const char* src = reinterpret_cast<const char*>(p.q + (it.t * p.H + it.hb * NH) * kKvQ);
-            const int bytes = min(NH, p.H - it.hb * NH) * 2 * kKvQ;
-            for (int at = (tid - kSoftThreads) * 128; at < bytes; at += kLoadWarps * 32 * 128)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
-            ok = wait(bar_q_free(q), (L::q_bufs == 2 ? n >> 1 : n) + 1) && wait(bar_c_free(n), (n >> 1) + 1);
-            if (!ok) break;
-            if constexpr (NH >= 2 * kLoadWarps)
-              stage_query_pairs<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
-                                    kLoadWarps, lane);
-            else
-              stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
-                                kLoadWarps, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_q(q));
-          }
-        }
       }
+      // the queries of a row whose first tile is next
+      if (ok && (i < 0 ? !first_ok : (word & kLast) != 0) && !(next_word & kStop)) {
+        item_of(it, static_cast<uint32_t>(next_item), p, g);
+        ++n;
+        const int q = L::q_bufs == 2 ? n & 1 : 0;
+        // on their way to L2 during the wait
+        const char* src = reinterpret_cast<const char*>(p.q + (it.t * p.H + it.hb * NH) * kKvQ);
+        const int bytes = min(NH, p.H - it.hb * NH) * 2 * kKvQ;
+        for (int at = (tid - kSoftThreads) * 128; at < bytes; at += kLoadWarps * 32 * 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
+        ok = wait(bar_q_free(q), (L::q_bufs == 2 ? n >> 1 : n) + 1) && wait(bar_c_free(n), (n >> 1) + 1);
+        if (!ok) break;
+        if constexpr (NH >= 2 * kLoadWarps)
+          stage_query_pairs<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
+                                kLoadWarps, lane);
+        else
+          stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps,
+                            lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q(q));
+      }
+      item = next_item;
       raw = next;
       word = next_word;
     }
@@ -564,7 +586,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     float* exch = reinterpret_cast<float*>(smem + L::off_p);  // [4 warps][NH], while P is not in use
     bool ok = true;
     int i = 0;
-    for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x, ++n) {
+    for (int n = 0;; ++n) {
+      // the next row's first tile, or the end; the same decision in all four warps
+      ok = wait(bar_full(i & 1, 0), i >> 1) && ok;
+      if (soft_bar_or(!ok || (s_n[i & 1] & kStop))) break;
+      const uint32_t item = static_cast<uint32_t>(s_k[i & 1]);
+      item_of(it, item, p, g);
       float2 c[C], m[C], l[C];  // factor to log2 units, negated reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         const int b = i & 1;
@@ -708,7 +735,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       if (tid < NH) {  // a head per thread
         const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
         if (g.splits > 1) {
-          g.part_ml[static_cast<int64_t>(it.k) * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_m[tid], sum);
+          g.part_ml[static_cast<int64_t>(item) * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_m[tid], sum);
         } else {
           s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
           if (p.lse && h0 + tid < p.H)
@@ -724,7 +751,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < NH / 8; ++j)
-            g.part_o[part_index<NH>(it.k, sh >> 1, warp, sh & 1, j, lane)] =
+            g.part_o[part_index<NH>(item, sh >> 1, warp, sh & 1, j, lane)] =
                 make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]), __uint_as_float(o[4 * j + 2]),
                             __uint_as_float(o[4 * j + 3]));
         }
@@ -849,6 +876,7 @@ cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, int sms, cudaStre
   constexpr int bytes = AttSmem<NH>::bytes;
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
+  if (g.next && (e = cudaMemsetAsync(g.next, 0, sizeof(uint32_t), st)) != cudaSuccess) return e;
   attend_kv4_kernel<NH><<<std::min(g.items, static_cast<uint32_t>(std::max(sms, 1))), kAttThreads, bytes, st>>>(p, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || g.splits == 1) return e;
@@ -866,9 +894,12 @@ cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, c
   if (p.H > 64) return launch_attend_kv4_pair(p, workspace, sms, st);
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(p.T * P.head_blocks * P.splits),
+  AttGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(p.T * P.head_blocks * P.splits), nullptr,
             reinterpret_cast<float4*>(ws + P.off_o),
             reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
+  // lists of unequal lengths: blocks take rows as they get free (501 rows of 16 heads and up to 1023 entries: 81 us,
+  // 88 us in turn; lists of one length cost the counter's clearing, 1 us)
+  if (g.items > static_cast<uint32_t>(sms)) g.next = reinterpret_cast<uint32_t*>(ws + 128);
   return P.NH == 16 ? launch_nh<16>(p, g, sms, st) : P.NH == 32 ? launch_nh<32>(p, g, sms, st) : launch_nh<64>(p, g, sms, st);
 }
 

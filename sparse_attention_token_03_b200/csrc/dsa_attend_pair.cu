@@ -16,7 +16,7 @@
 // heads move 3900 per block (operands of the MMAs 1920, decoding 1088, P 128,
 // the rest slots, queries and conflicts) for twice the products, in 5250
 // cycles against 36 x 53 + 16 x 65 = 2950 of MMAs.  2048 rows of 128 heads and
-// 2048 entries: 1.29 ms, 905 TFLOP/s (64-head blocks: 2.14 ms).
+// 2048 entries: 1.24 ms, 944 TFLOP/s (64-head blocks: 2.14 ms).
 //
 //   warps 0-3    softmax and output; a thread has one head and half of the keys
 //                (output dimensions), so maxima and sums need no shuffles
@@ -33,8 +33,8 @@
 // of the one before run as their operands become ready, K is refilled during O
 // and V during S.  The grid is persistent: a cluster takes every n-th row, and
 // the next row's queries, keys and scores proceed while the last one's output
-// is formed and stored.  That boundary still costs some 14000 cycles a row, of
-// which staging the queries behind the row's last score takes 11000.
+// is formed and stored.  What of that boundary still shows is the staging of the
+// queries behind the row's last score (some 7000 cycles a row).
 //
 // Numbers as in dsa_attend.cu: latents exact in fp16, queries fp16 after an
 // exact power of two, P fp16 relative to a reference that the scores pass by
