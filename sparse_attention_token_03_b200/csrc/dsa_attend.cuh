@@ -159,18 +159,6 @@ __device__ __forceinline__ void stg256(void* p, const uint32_t* r) {
                : "memory");
 }
 
-// Division of a position (below 2^31) by the page size as a product: with s =
-// ceil(log2 d) and mul = ceil(2^(31 + s) / d) the product's error n (mul d -
-// 2^(31 + s)) / (d 2^(31 + s)) is below 1 / d, so the quotient is exact.
-struct PageDiv {
-  uint32_t mul, shift;
-};
-inline PageDiv page_div(int d) {
-  uint32_t s = 0;
-  while ((int64_t(1) << s) < d) ++s;
-  return {static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
-}
-
 // Pool rows of four list entries of a sequence (its block table `table`), or -1
 // where nothing is listed or the position or page is outside its range, which
 // sets `bad`.  The four table loads are in flight together.
@@ -179,7 +167,7 @@ __device__ __forceinline__ void slots_of(const AttendParams& p, PageDiv div, con
   int blk[4], page[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    blk[k] = static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(max(pos[k], 0))) * div.mul >> div.shift);
+    blk[k] = div(max(pos[k], 0));
     page[k] = __ldg(table + min(blk[k], p.max_blocks - 1));
   }
 #pragma unroll

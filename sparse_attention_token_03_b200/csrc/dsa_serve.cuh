@@ -25,6 +25,21 @@ static_assert(kKvEntry == 416, "cache entry layout");
 // Row statistics of the index preparation (include/dsa_index.h, DSA_NORM_*).
 enum : int { kNormNone = 0, kNormRms = 1, kNormLayer = 2 };
 
+// Division of a position (below 2^31) by the page size as a product: with s =
+// ceil(log2 d) and mul = ceil(2^(31 + s) / d) the product's error n (mul d -
+// 2^(31 + s)) / (d 2^(31 + s)) is below 1 / d, so the quotient is exact.
+struct PageDiv {
+  uint32_t mul, shift;
+  __host__ __device__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul >> shift);
+  }
+};
+inline PageDiv page_div(int d) {
+  uint32_t s = 0;
+  while ((int64_t(1) << s) < d) ++s;
+  return {static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 struct TablesParams {
   const int32_t* cached_len;  // [B]
   const int32_t* new_len;     // [B]

@@ -130,3 +130,9 @@ def test_layout_replays_in_a_graph():
         for got, w in zip(outs, want[:5]):
             assert np.array_equal(got.cpu().numpy(), w)
         assert np.array_equal(tab.cpu().numpy(), want[6])
+
+
+@pytest.mark.parametrize("B,page,max_blocks", [(2049, 7, 3), (4095, 64, 2), (4096, 1, 5), (4097, 64, 2)])
+def test_layout_many_requests(B, page, max_blocks):
+    # up to and past the number of requests whose sums one block keeps
+    test_layout(B, page, max_blocks, True)
