@@ -98,3 +98,34 @@ def test_a_list_of_one_key_many_times():
     x = make(2, 128, 700, seed=23)
     x["idx"][:] = 17
     check(x)
+
+
+@pytest.mark.parametrize("T,H", [(200, 16), (160, 64), (100, 128)])
+def test_replays_with_more_rows_than_blocks(T, H):
+    # one workspace, replayed on changed inputs; the first row is padding in one of them
+    xs = [make(T, H, 200, B=2, ctx=400, seed=s, fill=f) for s, f in ((24, "ragged"), (25, "holes"))]
+    xs[1]["row_seq"][0] = -1
+    g = gpu(xs[0])
+    ws = torch.randint(0, 256, (dsa.dsa_attend_kv4_workspace_bytes(T, H, 200),), dtype=torch.uint8, device="cuda")
+    out, lse = dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, **g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dsa.dsa_attend_kv4(scale=SCALE, out=out, lse=lse, workspace=ws, **g)
+    for x in (xs[1], xs[0], xs[1]):
+        for k, v in gpu(x).items():
+            g[k].copy_(v)
+        out.fill_(5), lse.fill_(5)
+        graph.replay()
+        want = (torch.full_like(out, 5), torch.full_like(lse, 5))
+        dsa.dsa_attend_kv4(scale=SCALE, out=want[0], lse=want[1], **gpu(x))
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_one_sequence_table_and_long_lists():
+    # far more entries than a tile ring holds, most of them listing nothing
+    x = make(3, 24, 20000, ctx=3000, seed=26)
+    x["idx"][np.random.default_rng(26).random(x["idx"].shape) < 0.97] = -1
+    check(x)
+    y = make(2, 128, 20000, ctx=3000, seed=27)
+    y["idx"][:, 100:-100] = -1
+    check(y)
