@@ -251,17 +251,24 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
   }
 }
 
+template <bool FP8, bool INTER, int G>
+cudaError_t launch_groups(const PrepareParams& p, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>((p.T + G - 1) / G), G > 1 ? 1 : (p.H + kPrepRows - 1) / kPrepRows);
+  index_prepare_kernel<FP8, INTER, G, 1><<<grid, kPrepThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Tokens of a block: more share the weights' loads and the block's start, fewer
+// fill the GPU sooner.  With 64 heads, 300 tokens take 6.8 / 6.1 / 7.3 / 11.6 us
+// in groups of 1 / 2 / 4 / 8, 1000 tokens 16.3 / 12.0 / 9.7 / 12.1, 2000 tokens
+// - / 17.6 / 17.0 / 16.2.
 template <bool FP8, bool INTER>
 cudaError_t launch_prepare(const PrepareParams& p, int sms, cudaStream_t st) {
-  constexpr int kGroup = 8;
-  // groups of tokens when they fill the GPU, else 32 heads a block
-  if (p.T >= static_cast<int64_t>(sms) * kGroup)
-    index_prepare_kernel<FP8, INTER, kGroup, 1>
-        <<<static_cast<unsigned>((p.T + kGroup - 1) / kGroup), kPrepThreads, 0, st>>>(p);
-  else
-    index_prepare_kernel<FP8, INTER, 1, 1><<<dim3(static_cast<unsigned>(p.T), (p.H + kPrepRows - 1) / kPrepRows),
-                                             kPrepThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  const int64_t per_sm = p.T / std::max(sms, 1);
+  if (per_sm >= 8) return launch_groups<FP8, INTER, 8>(p, st);
+  if (per_sm >= 5) return launch_groups<FP8, INTER, 4>(p, st);
+  if (per_sm >= 2) return launch_groups<FP8, INTER, 2>(p, st);
+  return launch_groups<FP8, INTER, 1>(p, st);
 }
 
 }  // namespace

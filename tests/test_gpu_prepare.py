@@ -190,3 +190,9 @@ def test_prepare_many_tokens_in_place():
     b = call(x, False, False, q_out="in place")
     assert np.array_equal(a[0][:-7], b[0][:-7]) and np.array_equal(a[1], b[1])
     assert np.array_equal(b[0][-7:], ref.bf16_f64(x["q"])[-7:])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H,rot,norms", [(297, 33, 64, 0), (301, 64, 32, 1), (741, 5, 128, 2), (999, 40, 64, 1)])
+def test_prepare_tokens_in_small_groups(T, H, rot, norms, fp8):
+    test_prepare(T, H, rot, norms, False, fp8)
