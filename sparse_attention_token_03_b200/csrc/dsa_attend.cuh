@@ -86,11 +86,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // barrier (if `has`) has passed its phase.  A look at a barrier takes some 300
 // cycles while the tensor core reads shared memory, so a warp that needs
 // several in turn looks at all of them at once and only again for those that
-// were not ready.
+// were not ready.  The vote tells the other lanes that a phase is complete, but
+// orders no memory: __syncwarp hands them what the looking lane acquired.
 __device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
                                          volatile int* abort_flag, uint32_t* err) {
   if (!((ready >> which) & 1u)) {
     ready = __ballot_sync(~0u, has && mbar_test(bar, parity));
+    __syncwarp();
     if (!((ready >> which) & 1u)) {
       // the blocking look: polling would take the shared memory's time
       const bool ok = wait_bar(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, err);
