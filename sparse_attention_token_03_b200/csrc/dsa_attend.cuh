@@ -15,13 +15,46 @@ namespace dsa {
 constexpr float kRise = 8.f;  // log2 of the largest P before the reference moves
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
+// Looks at a barrier that warps of the partner block or an MMA over both blocks
+// arrive on (arrive_cluster, commit_pair_if): the acquiring fence has cluster
+// scope, restricted to shared memory, the only memory that the blocks of a pair
+// share (an unrestricted one would order the loads of cache entries too).
+__device__ __forceinline__ void acquire_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  acquire_cluster();
+  return ok != 0;
+}
+
 // mbar_wait in fewer instructions (the roles of these kernels wait at some
 // thirty places, and their loops share one instruction cache): the clock is
-// read and the abort flag looked at after every 256 tries.
+// read and the abort flag looked at after every 256 tries.  kPair: acquires at
+// cluster scope.
+template <bool kPair = false>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
   uint64_t t0 = 0;
 #pragma unroll 1
-  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+  for (uint32_t n = 1; !(kPair ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++n) {
     if (n & 255u) continue;
     const uint64_t now = globaltimer();
     if (t0 == 0) t0 = now;
@@ -32,6 +65,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
       return false;
     }
   }
+  if constexpr (kPair) acquire_cluster();
   return true;
 }
 
@@ -88,14 +122,15 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // several in turn looks at all of them at once and only again for those that
 // were not ready.  The vote tells the other lanes that a phase is complete, but
 // orders no memory: __syncwarp hands them what the looking lane acquired.
+template <bool kPair = false>
 __device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
                                          volatile int* abort_flag, uint32_t* err) {
   if (!((ready >> which) & 1u)) {
-    ready = __ballot_sync(~0u, has && mbar_test(bar, parity));
+    ready = __ballot_sync(~0u, has && (kPair ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)));
     __syncwarp();
     if (!((ready >> which) & 1u)) {
       // the blocking look: polling would take the shared memory's time
-      const bool ok = wait_bar(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, err);
+      const bool ok = wait_bar<kPair>(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, err);
       if (!__all_sync(~0u, ok)) return false;
       ready |= 1u << which;
     }

@@ -16,7 +16,8 @@
 // heads move 3900 per block (operands of the MMAs 1920, decoding 1088, P 128,
 // the rest slots, queries and conflicts) for twice the products, in 5250
 // cycles against 36 x 53 + 16 x 65 = 2950 of MMAs.  2048 rows of 128 heads and
-// 2048 entries: 1.24 ms, 944 TFLOP/s (64-head blocks: 2.14 ms).
+// 2048 entries: 1.35 ms in a burst of five calls, 867 TFLOP/s (64-head blocks:
+// 2.14 ms).
 //
 //   warps 0-3    softmax and output; a thread has one head and half of the keys
 //                (output dimensions), so maxima and sums need no shuffles
@@ -120,12 +121,16 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(bar));
   return r;
 }
-// Block scope is enough here and at every wait: the blocks share no data but
-// what the MMAs read, which the writer's proxy fence orders before its arrival.
-// (Release and acquire of cluster scope cost a fence over the block's global
-// loads each, 1.96 ms instead of 1.60 when it was measured.)
+// Arrives on a barrier of the cluster's first block.  What the warp wrote to
+// its own block's shared memory is released at cluster scope, since the first
+// block's MMAs read it; the fence is restricted to shared memory.  (With waits
+// to match, 2048 rows of 128 heads take 1.35 ms; 1.24 without the fences, which
+// the PTX memory model does not allow, 1.60 to 1.96 with unrestricted ones.)
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+      : "memory");
 }
 // Barrier over the two softmax warps of the same heads, with a predicate.
 __device__ __forceinline__ bool heads_bar_or(int id, bool v) {
@@ -239,9 +244,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   tc_fence_after();
 
   PairItem it{blockIdx.x >> 1, 0, 0, 0, 0};
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort, g.err)); };
+  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar<true>(bar(b), parity & 1u, s_abort, g.err)); };
+  // on a barrier that only this block's warps arrive on
+  auto wait_own = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort, g.err)); };
   // a tile's entry in the ring, for a warp that reads it
-  auto listed = [&](int i) { return wait(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
+  auto listed = [&](int i) { return wait_own(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
   auto taken = [&](int i) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarTaken + i % kPairRing));
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       uint4 v[2][3];
       load_query_row(v[0], p, item.t, h0 + r0, live(r0), lane);
       load_query_row(v[1], p, item.t, h0 + r0 + 1, live(r0 + 1), lane);
-      if (!wait(kBarQE, n + 1) || !wait(kBarCE, n + 1)) return false;
+      if (!wait(kBarQE, n + 1) || !wait_own(kBarCE, n + 1)) return false;
 #pragma unroll 1
       for (int r = r0;;) {
         const int two[2] = {r, r + 1};
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         publish(flags);
         ++tile;
         keys = 0;
-        ok = wait(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
+        ok = wait_own(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
       };
       int j0 = 0, j_hi = 0;  // the item's entries that are left
       const int32_t *table = nullptr, *list = nullptr;
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
           if (!((ready >> s) & 1u)) {
-            if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
+            if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
             tc_fence_after();
           }
           const uint64_t q0 = dQ + (2 * s * kBlk >> 4), k0 = dK + (2 * s * kBlk >> 4);
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
       commit_pair_if(leader, bar(kBarDrain));
       int unused = 0;
-      wait_bar(bar(kBarDrain), 0, &unused, g.err);
+      wait_bar<true>(bar(kBarDrain), 0, &unused, g.err);
       __syncwarp();
     } else if (warp == kMmaO && rank == 0) {
       // ------------------------------------------------- MMAs of the outputs
@@ -421,12 +428,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         // lane by lane: the four parts of V, the weights
         const uint32_t mine = bar(lane == 4 ? kBarP : kBarVF + (lane & 3));
         uint32_t ready = 0;
-        if (!wait_any(ready, 4, lane < 5, mine, i & 1, s_abort, g.err)) break;
+        if (!wait_any<true>(ready, 4, lane < 5, mine, i & 1, s_abort, g.err)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           if (!((ready >> u) & 1u)) {
-            if (!(ok = wait_any(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
+            if (!(ok = wait_any<true>(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
             tc_fence_after();
           }
           const uint64_t a0 = dP + (((u >> 1) * kBlk + 64 * (u & 1)) >> 4), b0 = dV + (2 * u * 2048 >> 4);
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       }
       commit_pair_if(leader, bar(kBarDrain + 1));
       int unused = 0;
-      wait_bar(bar(kBarDrain + 1), 0, &unused, g.err);
+      wait_bar<true>(bar(kBarDrain + 1), 0, &unused, g.err);
       __syncwarp();
     }
   } else if (warp >= kQ) {
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         uint32_t ready = 0;  // of the four parts
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
-          if (!(ok = wait_any(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort, g.err))) break;
+          if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort, g.err))) break;
           if (s == 0) {
             const uint32_t dst = sK + 8 * kBlk + key * 128;
             sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         }
         ok = wait(kBarS + (i & 1), static_cast<uint32_t>(i >> 1)) && ok;
         if (first) {
-          ok = wait(kBarCF, n) && ok;
+          ok = wait_own(kBarCF, n) && ok;
           c = s_c[row];
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(kBarCE));
