@@ -377,7 +377,8 @@ DSA_API int dsa_index_device_status(const void* workspace, uint32_t* status, voi
  *  - `status` is a device word of the caller's, or NULL.  A call ORs the bits
  *    of dsa_index_device_status into it and never clears it, so one word can
  *    collect a whole step; without it the same checks skip the same accesses
- *    but go unreported.
+ *    but go unreported (dsa_attend_kv4 has a workspace, whose status word holds
+ *    the bits of its latest call either way).
  *  - A row with position < 0, slot < 0 or sequence < 0 is padding (the rows
  *    of a captured graph behind the last token): its outputs are left as
  *    they were.
@@ -518,7 +519,10 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  *   workspace    device, 256-byte aligned, of
  *                dsa_attend_kv4_workspace_bytes(T, H, n) bytes
  *                (of the current device); calls that may run at the same time
- *                need workspaces of their own
+ *                need workspaces of their own.  Its first word is the call's
+ *                status word, with or without `status`:
+ *                dsa_index_device_status(workspace) reads the latest call's
+ *                (bit 0, a wait that gave up, leaves outputs unspecified)
  * Scores, softmax statistics and output sums are fp32.  Results do not depend
  * on the rest of the batch's contents.  T == 0 is a no-op.  Requires
  * max_blocks * page_size < 2^31, n_pages * page_size < 2^31, T * H < 2^31.

@@ -816,7 +816,8 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
     idx (T, n) int32: positions within the row's sequence (out_idx of the
     index calls), negative entries skipped.  row_seq (T,) int32 names each
     row's sequence (< 0: padding, left as it was); without it row t reads
-    sequence t.  Returns (out (T, H, 512) bf16, lse (T, H) fp32).
+    sequence t.  With or without `status`, the status bits of the latest call on
+    a workspace are read by dsa_index_device_status(workspace).  Returns (out (T, H, 512) bf16, lse (T, H) fp32).
     """
     r = _native().attend(q, kv_pages, block_table, idx, float(scale), row_seq, out, lse, workspace, status)
     if type(r) is tuple:

@@ -116,7 +116,7 @@ struct AttGrid {
                                    // the blocks' first ones that are taken
   float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
   float2* part_ml;                 // [T][head_blocks][splits][NH]
-  uint32_t* err;
+  uint32_t* err;                   // the workspace's status word
   PageDiv div;
 };
 
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto wait = [&](uint32_t bar, int parity) {
-    return __all_sync(~0u, wait_bar(bar, static_cast<uint32_t>(parity) & 1u, s_abort, g.err));
+    return __all_sync(~0u, wait_bar(bar, static_cast<uint32_t>(parity) & 1u, s_abort));
   };
 
   if (tid == 0) {
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         ++n;
       }
       if (ok) publish(kStop);
-      if (__any_sync(~0u, bad) && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
+      if (__any_sync(~0u, bad) && lane == 0) report(p, g.err, kErrOverflow);
     } else if (warp == kMmaWarp || warp == kMmaOddWarp) {
       // -------------------------------------------------- MMAs of the scores
       // One warp for each tile buffer: 36 MMAs take a warp longer to issue than
@@ -428,18 +428,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         const uint32_t mine = lane == 4 ? bar_read(b) : bar_full(b, lane & 3);
         const uint32_t par = static_cast<uint32_t>(lane == 4 ? k + 1 : k) & 1u;
         uint32_t ready = 0;
-        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, g.err))) break;
+        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort))) break;
         const int word = s_n[b];
         if (word & kStop) break;
         const int n = word >> kRowShift, q = L::q_bufs == 2 ? n & 1 : 0;
         if (!(ok = wait(bar_q(q), L::q_bufs == 2 ? n >> 1 : n))) break;
-        if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort, g.err))) break;
+        if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort))) break;
         tc_fence_after();
         const uint64_t dQ = smem_desc_sw128(sbase + q * L::q_bytes);
 #pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
           if (!((ready >> s) & 1u)) {
-            if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, g.err))) break;
+            if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort))) break;
             tc_fence_after();
           }
           const uint64_t k0 = dK + (2 * s * kBlockBytes >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       const uint32_t drain = bar_drain + (b ? 16 : 0);
       commit_if(leader, drain);
       int unused = 0;
-      wait_bar(drain, 0, &unused, g.err);
+      if (!wait_bar(drain, 0, &unused)) *s_abort = 1;
       __syncwarp();
     } else if (warp == kMmaOWarp) {
       // ------------------------------------------------- MMAs of the outputs
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       }
       commit_if(leader, bar_drain + 8);
       int unused = 0;
-      wait_bar(bar_drain + 8, 0, &unused, g.err);
+      if (!wait_bar(bar_drain + 8, 0, &unused)) *s_abort = 1;
       __syncwarp();
     }
   } else if (warp >= kSoftWarps) {
@@ -781,6 +781,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
     }
   }
   __syncthreads();
+  if (tid == 0 && *s_abort) report(p, g.err, kErrTimeout);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(*s_tmem, kTmemCols);
@@ -860,9 +861,9 @@ AttPlan plan_attend(int64_t T, int H, int n, int sms) {
   // fewer rows than SMs: parts of at least two tiles (one row of 64 heads and 2048 entries: 21.6 us in 16 parts,
   // 25 us in 32 of one tile, whose partial outputs cost more than their tile)
   P.splits = items >= sms || items == 0 ? 1 : static_cast<int>(std::min<int64_t>(sms / items, (P.tiles + 1) / 2));
-  P.off_ml = 256;
+  P.off_ml = kAttHeader;
   P.off_o = P.off_ml;
-  P.bytes = 256;
+  P.bytes = kAttHeader;
   if (P.splits > 1) {
     const size_t rows = static_cast<size_t>(items) * P.splits * P.NH;
     P.off_o = (P.off_ml + rows * sizeof(float2) + 255) / 256 * 256;
@@ -876,7 +877,7 @@ cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, int sms, cudaStre
   constexpr int bytes = AttSmem<NH>::bytes;
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  if (g.next && (e = cudaMemsetAsync(g.next, 0, sizeof(uint32_t), st)) != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(g.err, 0, kAttHeader, st)) != cudaSuccess) return e;  // status word and counter
   attend_kv4_kernel<NH><<<std::min(g.items, static_cast<uint32_t>(std::max(sms, 1))), kAttThreads, bytes, st>>>(p, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || g.splits == 1) return e;
@@ -896,10 +897,10 @@ cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, c
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   AttGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(p.T * P.head_blocks * P.splits), nullptr,
             reinterpret_cast<float4*>(ws + P.off_o),
-            reinterpret_cast<float2*>(ws + P.off_ml), p.status ? p.status : reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
+            reinterpret_cast<float2*>(ws + P.off_ml), reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
   // lists of unequal lengths: blocks take rows as they get free (501 rows of 16 heads and up to 1023 entries: 81 us,
-  // 88 us in turn; lists of one length cost the counter's clearing, 1 us)
-  if (g.items > static_cast<uint32_t>(sms)) g.next = reinterpret_cast<uint32_t*>(ws + 128);
+  // 88 us in turn)
+  if (g.items > static_cast<uint32_t>(sms)) g.next = reinterpret_cast<uint32_t*>(ws + kAttCounter);
   return P.NH == 16 ? launch_nh<16>(p, g, sms, st) : P.NH == 32 ? launch_nh<32>(p, g, sms, st) : launch_nh<64>(p, g, sms, st);
 }
 

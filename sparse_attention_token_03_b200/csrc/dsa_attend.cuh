@@ -12,8 +12,16 @@
 
 namespace dsa {
 
+constexpr int kAttHeader = 256, kAttCounter = 128;  // bytes: start of a workspace, cleared by a launch: status word, row counter
 constexpr float kRise = 8.f;  // log2 of the largest P before the reference moves
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+
+// Status bits of a call: into its workspace's word, which the launch clears, and
+// into the caller's.
+__device__ __forceinline__ void report(const AttendParams& p, uint32_t* word, uint32_t bits) {
+  atomicOr(word, bits);
+  if (p.status) atomicOr(p.status, bits);
+}
 
 // Looks at a barrier that warps of the partner block or an MMA over both blocks
 // arrive on (arrive_cluster, commit_pair_if): the acquiring fence has cluster
@@ -47,11 +55,12 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 }
 
 // mbar_wait in fewer instructions (the roles of these kernels wait at some
-// thirty places, and their loops share one instruction cache): the clock is
-// read and the abort flag looked at after every 256 tries.  kPair: acquires at
-// cluster scope.
+// thirty places, and their loops share one instruction cache: the clock is
+// read and the abort flag looked at after every 256 tries; a wait that gives up
+// sets the flag, which the kernel reports at its end).  kPair: acquires at cluster
+// scope.
 template <bool kPair = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t n = 1; !(kPair ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++n) {
@@ -61,7 +70,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     if (*abort_flag) return false;
     if (now - t0 > kWaitTimeoutNs) {
       *abort_flag = 1;
-      atomicOr(err, kErrTimeout);
       return false;
     }
   }
@@ -124,13 +132,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // orders no memory: __syncwarp hands them what the looking lane acquired.
 template <bool kPair = false>
 __device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
-                                         volatile int* abort_flag, uint32_t* err) {
+                                         volatile int* abort_flag) {
   if (!((ready >> which) & 1u)) {
     ready = __ballot_sync(~0u, has && (kPair ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)));
     __syncwarp();
     if (!((ready >> which) & 1u)) {
       // the blocking look: polling would take the shared memory's time
-      const bool ok = wait_bar<kPair>(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, err);
+      const bool ok = wait_bar<kPair>(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag);
       if (!__all_sync(~0u, ok)) return false;
       ready |= 1u << which;
     }

@@ -83,7 +83,7 @@ struct PairGrid {
   uint32_t items;                  // T * head_blocks * splits, below 2^31
   float* part_o;                   // [items][128][512]
   float2* part_ml;                 // [items][128]
-  uint32_t* err;
+  uint32_t* err;                   // the workspace's status word
   PageDiv div;
   bool out32;                      // out is 32-byte aligned
 };
@@ -94,7 +94,7 @@ struct PairItem {
   int64_t t;
   int hb, split, seq;
 };
-__device__ __forceinline__ bool next_item(PairItem& it, const AttendParams& p, const PairGrid& g, bool report) {
+__device__ __forceinline__ bool next_item(PairItem& it, const AttendParams& p, const PairGrid& g, bool tell) {
   for (; it.k < g.items; it.k += gridDim.x >> 1) {
     const uint32_t row = it.k / static_cast<uint32_t>(g.splits);
     it.split = static_cast<int>(it.k - row * g.splits);
@@ -102,7 +102,7 @@ __device__ __forceinline__ bool next_item(PairItem& it, const AttendParams& p, c
     it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
     it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
     if (it.seq >= 0 && it.seq < p.B) return true;
-    if (it.seq >= p.B && report && p.status) atomicOr(p.status, kErrOverflow);  // else padding
+    if (it.seq >= p.B && tell) report(p, g.err, kErrOverflow);  // else padding
   }
   return false;
 }
@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   tc_fence_after();
 
   PairItem it{blockIdx.x >> 1, 0, 0, 0, 0};
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar<true>(bar(b), parity & 1u, s_abort, g.err)); };
+  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar<true>(bar(b), parity & 1u, s_abort)); };
   // on a barrier that only this block's warps arrive on
-  auto wait_own = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort, g.err)); };
+  auto wait_own = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort)); };
   // a tile's entry in the ring, for a warp that reads it
   auto listed = [&](int i) { return wait_own(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
   auto taken = [&](int i) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         if (ok) turn(kLast | (first ? kFirst : 0));  // without keys where nothing is listed
       }
       if (ok) publish(kStop);
-      if (__any_sync(~0u, bad) && rank == 0 && lane == 0 && p.status) atomicOr(p.status, kErrOverflow);
+      if (__any_sync(~0u, bad) && rank == 0 && lane == 0) report(p, g.err, kErrOverflow);
     } else if (warp == kMma && rank == 0) {
       // -------------------------------------------------- MMAs of the scores
       constexpr uint32_t tmem = 0;  // all 512 columns are allocated
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
           if (!((ready >> s) & 1u)) {
-            if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, g.err))) break;
+            if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort))) break;
             tc_fence_after();
           }
           const uint64_t q0 = dQ + (2 * s * kBlk >> 4), k0 = dK + (2 * s * kBlk >> 4);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
       commit_pair_if(leader, bar(kBarDrain));
       int unused = 0;
-      wait_bar<true>(bar(kBarDrain), 0, &unused, g.err);
+      if (!wait_bar<true>(bar(kBarDrain), 0, &unused)) *s_abort = 1;
       __syncwarp();
     } else if (warp == kMmaO && rank == 0) {
       // ------------------------------------------------- MMAs of the outputs
@@ -428,12 +428,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         // lane by lane: the four parts of V, the weights
         const uint32_t mine = bar(lane == 4 ? kBarP : kBarVF + (lane & 3));
         uint32_t ready = 0;
-        if (!wait_any<true>(ready, 4, lane < 5, mine, i & 1, s_abort, g.err)) break;
+        if (!wait_any<true>(ready, 4, lane < 5, mine, i & 1, s_abort)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           if (!((ready >> u) & 1u)) {
-            if (!(ok = wait_any<true>(ready, u, lane < 5, mine, i & 1, s_abort, g.err))) break;
+            if (!(ok = wait_any<true>(ready, u, lane < 5, mine, i & 1, s_abort))) break;
             tc_fence_after();
           }
           const uint64_t a0 = dP + (((u >> 1) * kBlk + 64 * (u & 1)) >> 4), b0 = dV + (2 * u * 2048 >> 4);
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       }
       commit_pair_if(leader, bar(kBarDrain + 1));
       int unused = 0;
-      wait_bar<true>(bar(kBarDrain + 1), 0, &unused, g.err);
+      if (!wait_bar<true>(bar(kBarDrain + 1), 0, &unused)) *s_abort = 1;
       __syncwarp();
     }
   } else if (warp >= kQ) {
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         uint32_t ready = 0;  // of the four parts
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
-          if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort, g.err))) break;
+          if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort))) break;
           if (s == 0) {
             const uint32_t dst = sK + 8 * kBlk + key * 128;
             sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);
@@ -712,6 +712,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   // a block's memory and barriers are in use until its partner is done too
   __syncwarp();
   cluster_sync();
+  if (tid == 0 && *s_abort) report(p, g.err, kErrTimeout);
   if (warp == kMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(*s_tmem) : "memory");
@@ -763,10 +764,10 @@ PairPlan plan_pair(int64_t T, int H, int n, int sms) {
   const int64_t rows = T * P.head_blocks, clusters = std::max(sms / 2, 1);
   P.splits = rows >= clusters || rows == 0 ? 1 : static_cast<int>(std::min<int64_t>(clusters / rows, P.tiles));
   P.items = rows * P.splits;
-  P.bytes = 256;
+  P.bytes = kAttHeader;
   if (P.splits > 1) {
     const size_t part_rows = static_cast<size_t>(P.items) * 2 * kHalf;
-    P.off_o = (256 + part_rows * sizeof(float2) + 255) / 256 * 256;
+    P.off_o = (kAttHeader + part_rows * sizeof(float2) + 255) / 256 * 256;
     P.bytes = P.off_o + part_rows * kKvLat * sizeof(float);
   }
   return P;
@@ -780,10 +781,11 @@ cudaError_t launch_attend_kv4_pair(const AttendParams& p, void* workspace, int s
   const PairPlan P = plan_pair(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PairGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(P.items), reinterpret_cast<float*>(ws + P.off_o),
-             reinterpret_cast<float2*>(ws + 256), p.status ? p.status : reinterpret_cast<uint32_t*>(ws),
+             reinterpret_cast<float2*>(ws + kAttHeader), reinterpret_cast<uint32_t*>(ws),
              page_div(p.page_size), reinterpret_cast<uintptr_t>(p.out) % 32 == 0};
   cudaError_t e = cudaFuncSetAttribute(attend_kv4_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e != cudaSuccess) return e;
+  if ((e = cudaMemsetAsync(g.err, 0, kAttHeader, st)) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<int64_t>(P.items, std::max(sms / 2, 1))));
   cfg.blockDim = dim3(kPairThreads);

@@ -143,3 +143,25 @@ def test_many_calls_give_the_same_bits(T, H):
         dsa.dsa_attend_kv4(scale=SCALE, out=out, lse=lse, **g)
         off += (out != want[0]).sum() + (lse != want[1]).sum()
     assert int(off) == 0
+
+
+@pytest.mark.parametrize("T,H", [(4, 16), (4, 128), (200, 16), (200, 128)])
+def test_workspace_has_the_calls_status_word(T, H):
+    # with and without a status word of the caller's, from a workspace of garbage; a later good call clears it
+    x = make(T, H, 130, B=4, ctx=500, seed=8 + T)
+    ws = torch.full((max(256, dsa.dsa_attend_kv4_workspace_bytes(T, H, 130)),), 0xA5, dtype=torch.uint8, device="cuda")
+    assert dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, **gpu(x)) and dsa.dsa_index_device_status(ws) == 0
+    y = dict(x, idx=x["idx"].copy())
+    y["idx"][T - 1, 7] = 2 ** 31 - 1                    # past the table
+    z = dict(x, row_seq=x["row_seq"].copy())
+    z["row_seq"][T // 2] = 4                            # no such sequence
+    w = dict(x, table=x["table"].copy())
+    w["table"][:, 1] = -7                               # no such page
+    for bad in (y, z, w):
+        dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, **gpu(bad))
+        assert dsa.dsa_index_device_status(ws) == 2
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, status=st, **gpu(bad))
+        assert dsa.dsa_index_device_status(ws) == 2 and int(st) == 2
+        dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, status=st, **gpu(x))
+        assert dsa.dsa_index_device_status(ws) == 0 and int(st) == 2       # the caller's word collects
