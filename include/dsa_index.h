@@ -536,8 +536,10 @@ DSA_API int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n
 /*
  * Failure injection for tests of the bounded device waits (no counterpart on
  * the pages).  Arms a one-shot fault for the calling host thread: the next
- * fused scoring launch of any entry point issues no loads, so its MMA warp
- * waits for data that never arrives; that wait gives up after limit_ns
+ * fused scoring launch of any entry point issues no loads, or the next launch
+ * of dsa_attend_kv4 stops handing out its lists behind their first tiles
+ * (whichever comes first), so that warps wait for data that never arrives;
+ * those waits give up after limit_ns
  * (1 ms .. 2 s), the kernel unwinds (in-flight copies and tensor-core work
  * drained, tensor memory released), sets bit 0 of the device status word and
  * returns.  The call's outputs are then unspecified; later calls are

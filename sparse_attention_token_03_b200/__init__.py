@@ -858,7 +858,7 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
 
 def dsa_test_inject_wait_timeout(limit_ns: int) -> None:
     """Arm a one-shot injected wait timeout for the calling thread's next
-    scoring launch (tests of the bounded-wait failure path)."""
+    scoring or attention launch (tests of the bounded-wait failure path)."""
     _check(lib().dsa_test_inject_wait_timeout(int(limit_ns)))
 
 

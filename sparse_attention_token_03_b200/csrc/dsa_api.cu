@@ -153,8 +153,9 @@ void prof_mark(cudaStream_t st, const char* kernel) {
 }
 
 // One-shot failure injection armed by dsa_test_inject_wait_timeout (per
-// host thread): the next fused-kernel launch withholds its loads and limits
-// its pipeline waits, so that a wait runs out on the device.
+// host thread): the next fused scoring launch withholds its loads, or the next
+// attention launch its lists, and limits its waits, so that one runs out on the
+// device.
 struct WaitInjection {
   bool armed = false;
   uint64_t limit_ns = 0;
@@ -1542,6 +1543,11 @@ int dsa_attend_kv4(const uint16_t* q, const uint8_t* kv_pages, int64_t n_pages, 
   if (ws_bytes < need) return fail(DSA_EWORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   AttendParams p{q, kv_pages, n_pages, page_size, block_table, B, max_blocks, row_seq, idx, T, H, n, scale, out, lse,
                  status};
+  if (g_inject.armed) {
+    g_inject.armed = false;
+    p.wait_ns = g_inject.limit_ns;
+    p.hold_tiles = 2;  // the first one is worked on
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(st);
   cudaError_t e = launch_attend_kv4(p, workspace, sm_count(), st);

@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto wait = [&](uint32_t bar, int parity) {
-    return __all_sync(~0u, wait_bar(bar, static_cast<uint32_t>(parity) & 1u, s_abort));
+    return __all_sync(~0u, wait_bar(bar, static_cast<uint32_t>(parity) & 1u, s_abort, p.wait_ns));
   };
 
   if (tid == 0) {
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         publish(flags);
         ++tile;
         keys = 0;
-        ok = wait(bar_taken(tile % kRing), tile / kRing + 1);
+        ok = wait(bar_taken(tile % kRing), tile / kRing + 1) && tile < p.hold_tiles;
       };
       int j0 = 0, j_hi = 0, pos[4];  // the item's entries that are left
       const int32_t* list = nullptr;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         if (ok) turn(row | kLast);
         ++n;
       }
-      if (ok) publish(kStop);
+      if (ok && tile + 1 < p.hold_tiles) publish(kStop);
       if (__any_sync(~0u, bad) && lane == 0) report(p, g.err, kErrOverflow);
     } else if (warp == kMmaWarp || warp == kMmaOddWarp) {
       // -------------------------------------------------- MMAs of the scores
@@ -428,18 +428,18 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         const uint32_t mine = lane == 4 ? bar_read(b) : bar_full(b, lane & 3);
         const uint32_t par = static_cast<uint32_t>(lane == 4 ? k + 1 : k) & 1u;
         uint32_t ready = 0;
-        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort))) break;
+        if (!(ok = wait_any(ready, 0, lane < 5, mine, par, s_abort, p.wait_ns))) break;
         const int word = s_n[b];
         if (word & kStop) break;
         const int n = word >> kRowShift, q = L::q_bufs == 2 ? n & 1 : 0;
         if (!(ok = wait(bar_q(q), L::q_bufs == 2 ? n >> 1 : n))) break;
-        if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort))) break;
+        if (!(ok = wait_any(ready, 4, lane < 5, mine, par, s_abort, p.wait_ns))) break;
         tc_fence_after();
         const uint64_t dQ = smem_desc_sw128(sbase + q * L::q_bytes);
 #pragma unroll 1
         for (int s = 0; s < kParts; ++s) {
           if (!((ready >> s) & 1u)) {
-            if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort))) break;
+            if (!(ok = wait_any(ready, s, lane < 5, mine, par, s_abort, p.wait_ns))) break;
             tc_fence_after();
           }
           const uint64_t k0 = dK + (2 * s * kBlockBytes >> 4), q0 = dQ + (2 * s * L::q_block >> 4);
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       const uint32_t drain = bar_drain + (b ? 16 : 0);
       commit_if(leader, drain);
       int unused = 0;
-      if (!wait_bar(drain, 0, &unused)) *s_abort = 1;
+      if (!wait_bar(drain, 0, &unused, p.wait_ns)) *s_abort = 1;
       __syncwarp();
     } else if (warp == kMmaOWarp) {
       // ------------------------------------------------- MMAs of the outputs
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       }
       commit_if(leader, bar_drain + 8);
       int unused = 0;
-      if (!wait_bar(bar_drain + 8, 0, &unused)) *s_abort = 1;
+      if (!wait_bar(bar_drain + 8, 0, &unused, p.wait_ns)) *s_abort = 1;
       __syncwarp();
     }
   } else if (warp >= kSoftWarps) {

@@ -60,7 +60,7 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
 // sets the flag, which the kernel reports at its end).  kPair: acquires at cluster
 // scope.
 template <bool kPair = false>
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns) {
   uint64_t t0 = 0;
 #pragma unroll 1
   for (uint32_t n = 1; !(kPair ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++n) {
@@ -68,7 +68,7 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     const uint64_t now = globaltimer();
     if (t0 == 0) t0 = now;
     if (*abort_flag) return false;
-    if (now - t0 > kWaitTimeoutNs) {
+    if (now - t0 > limit_ns) {
       *abort_flag = 1;
       return false;
     }
@@ -132,13 +132,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // orders no memory: __syncwarp hands them what the looking lane acquired.
 template <bool kPair = false>
 __device__ __forceinline__ bool wait_any(uint32_t& ready, int which, bool has, uint32_t bar, uint32_t parity,
-                                         volatile int* abort_flag) {
+                                         volatile int* abort_flag, uint64_t limit_ns) {
   if (!((ready >> which) & 1u)) {
     ready = __ballot_sync(~0u, has && (kPair ? mbar_test_cluster(bar, parity) : mbar_test(bar, parity)));
     __syncwarp();
     if (!((ready >> which) & 1u)) {
       // the blocking look: polling would take the shared memory's time
-      const bool ok = wait_bar<kPair>(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag);
+      const bool ok = wait_bar<kPair>(__shfl_sync(~0u, bar, which), __shfl_sync(~0u, parity, which), abort_flag, limit_ns);
       if (!__all_sync(~0u, ok)) return false;
       ready |= 1u << which;
     }

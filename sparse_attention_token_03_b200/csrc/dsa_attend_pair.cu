@@ -244,9 +244,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
   tc_fence_after();
 
   PairItem it{blockIdx.x >> 1, 0, 0, 0, 0};
-  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar<true>(bar(b), parity & 1u, s_abort)); };
+  auto wait = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar<true>(bar(b), parity & 1u, s_abort, p.wait_ns)); };
   // on a barrier that only this block's warps arrive on
-  auto wait_own = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort)); };
+  auto wait_own = [&](int b, uint32_t parity) { return __all_sync(~0u, wait_bar(bar(b), parity & 1u, s_abort, p.wait_ns)); };
   // a tile's entry in the ring, for a warp that reads it
   auto listed = [&](int i) { return wait_own(kBarListed + i % kPairRing, static_cast<uint32_t>(i / kPairRing)); };
   auto taken = [&](int i) {
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         publish(flags);
         ++tile;
         keys = 0;
-        ok = wait_own(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u);
+        ok = wait_own(kBarTaken + tile % kPairRing, static_cast<uint32_t>(tile / kPairRing) + 1u) && tile < p.hold_tiles;
       };
       int j0 = 0, j_hi = 0;  // the item's entries that are left
       const int32_t *table = nullptr, *list = nullptr;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         it.k += gridDim.x >> 1;
         if (ok) turn(kLast | (first ? kFirst : 0));  // without keys where nothing is listed
       }
-      if (ok) publish(kStop);
+      if (ok && tile + 1 < p.hold_tiles) publish(kStop);
       if (__any_sync(~0u, bad) && rank == 0 && lane == 0) report(p, g.err, kErrOverflow);
     } else if (warp == kMma && rank == 0) {
       // -------------------------------------------------- MMAs of the scores
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
           if (!((ready >> s) & 1u)) {
-            if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort))) break;
+            if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKF + (lane & 3)), i & 1, s_abort, p.wait_ns))) break;
             tc_fence_after();
           }
           const uint64_t q0 = dQ + (2 * s * kBlk >> 4), k0 = dK + (2 * s * kBlk >> 4);
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       // nothing may be in flight when the tensor memory is freed (also after a wait that gave up)
       commit_pair_if(leader, bar(kBarDrain));
       int unused = 0;
-      if (!wait_bar<true>(bar(kBarDrain), 0, &unused)) *s_abort = 1;
+      if (!wait_bar<true>(bar(kBarDrain), 0, &unused, p.wait_ns)) *s_abort = 1;
       __syncwarp();
     } else if (warp == kMmaO && rank == 0) {
       // ------------------------------------------------- MMAs of the outputs
@@ -428,12 +428,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         // lane by lane: the four parts of V, the weights
         const uint32_t mine = bar(lane == 4 ? kBarP : kBarVF + (lane & 3));
         uint32_t ready = 0;
-        if (!wait_any<true>(ready, 4, lane < 5, mine, i & 1, s_abort)) break;
+        if (!wait_any<true>(ready, 4, lane < 5, mine, i & 1, s_abort, p.wait_ns)) break;
         tc_fence_after();
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
           if (!((ready >> u) & 1u)) {
-            if (!(ok = wait_any<true>(ready, u, lane < 5, mine, i & 1, s_abort))) break;
+            if (!(ok = wait_any<true>(ready, u, lane < 5, mine, i & 1, s_abort, p.wait_ns))) break;
             tc_fence_after();
           }
           const uint64_t a0 = dP + (((u >> 1) * kBlk + 64 * (u & 1)) >> 4), b0 = dV + (2 * u * 2048 >> 4);
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       }
       commit_pair_if(leader, bar(kBarDrain + 1));
       int unused = 0;
-      if (!wait_bar<true>(bar(kBarDrain + 1), 0, &unused)) *s_abort = 1;
+      if (!wait_bar<true>(bar(kBarDrain + 1), 0, &unused, p.wait_ns)) *s_abort = 1;
       __syncwarp();
     }
   } else if (warp >= kQ) {
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         uint32_t ready = 0;  // of the four parts
 #pragma unroll 1
         for (int s = 0; s < 4; ++s) {
-          if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort))) break;
+          if (!(ok = wait_any<true>(ready, s, lane < 4, bar(kBarKE + (lane & 3)), (i + 1) & 1, s_abort, p.wait_ns))) break;
           if (s == 0) {
             const uint32_t dst = sK + 8 * kBlk + key * 128;
             sts128(dst + (((2 * part) ^ sw) << 4), rope[0], rope[1], rope[2], rope[3]);

@@ -7,6 +7,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "dsa_ptx.cuh"
+
 namespace dsa {
 
 // One cached token of the 4-bit latent cache, 416 bytes: 512 E2M1 codes (two
@@ -116,6 +118,10 @@ struct AttendParams {
   uint16_t* out;               // [T][H][512] bf16
   float* lse;                  // [T][H] or null
   uint32_t* status;            // may be null
+  // limit of a wait, and the tiles that a block's list warp hands out before it
+  // stops as if it had died (no limit but in tests: dsa_test_inject_wait_timeout)
+  uint64_t wait_ns = kWaitTimeoutNs;
+  int hold_tiles = INT32_MAX;
 };
 size_t attend_workspace_bytes(int64_t T, int H, int n, int sms);
 cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, cudaStream_t st);
