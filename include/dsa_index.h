@@ -523,7 +523,12 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  *                status word, with or without `status`:
  *                dsa_index_device_status(workspace) reads the latest call's
  *                (bit 0, a wait that gave up, leaves outputs unspecified)
- * Scores, softmax statistics and output sums are fp32.  Results do not depend
+ * Scores, softmax statistics and output sums are fp32.  The weights that
+ * multiply the latents are fp16, relative to a score at most 8 log 2 below the
+ * largest one of the row (or of its part, where the list is split): 2^-11 of a
+ * weight, or 2^-32 of that reference's weight where that is more, so that the
+ * small weights of a list move out by at most n 2^-32 max |latent|; lse takes
+ * them in fp32.  Results do not depend
  * on the rest of the batch's contents.  T == 0 is a no-op.  Requires
  * max_blocks * page_size < 2^31, n_pages * page_size < 2^31, T * H < 2^31.
  */

@@ -56,9 +56,11 @@
 // rotary parts multiply as bf16 (same power of two, exact).  P is fp16, 2^-11
 // relative (bf16's 2^-8 would double the output's error).  exp2 is taken
 // relative to a reference per head, the maximum of the first tile, that moves
-// to the running maximum when a score passes it by 2^8, so P stays at most 256
-// and O^T in TMEM is rescaled only then, which ordinary score distributions
-// never need.  Scores, sums and O^T are fp32.
+// to the running maximum when a weight passes the reference's by 2^8, so O^T in
+// TMEM is rescaled only then, which ordinary score distributions never need.
+// All weights carry a factor of 2^7, so that they fill fp16's range: at most
+// 2^15, and each off by at most 2^-32 of the reference's below its normal range.
+// The sums take the unrounded weights.  Scores, sums and O^T are fp32.
 //
 // Few rows: the list is split over blocks, each writes its fp32 O and (m, l),
 // and a second kernel joins them.
@@ -95,7 +97,7 @@ struct AttSmem {
   static constexpr uint32_t off_p = off_k + 2 * kTileBytes;
   static constexpr uint32_t off_c = off_p + kKt * 128;   // [2 rows] per head: factor of a score in log2 units
   static constexpr uint32_t off_f = off_c + 2 * NH * 4;  // per head: rescaling factor, then 1 / sum
-  static constexpr uint32_t off_m = off_f + NH * 4;      // per head: reference, for the statistics
+  static constexpr uint32_t off_m = off_f + NH * 4;      // per head: reference less kLift, for the statistics
   static constexpr uint32_t off_ring = off_m + NH * 4;   // pool rows of the next tiles' keys
   static constexpr uint32_t off_count = off_ring + kRing * kKt * 4;  // words of the ring tiles, then of the buffers
   static constexpr uint32_t off_bars = off_count + 2 * (kRing + 2) * 4;  // and their items
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       if (soft_bar_or(!ok || (s_n[i & 1] & kStop))) break;
       const uint32_t item = static_cast<uint32_t>(s_k[i & 1]);
       item_of(it, item, p, g);
-      float2 c[C], m[C], l[C];  // factor to log2 units, negated reference (from the first tile on), sum
+      float2 c[C], m[C], l[C];  // factor to log2 units, kLift less the reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         const int b = i & 1;
         ok = wait(bar_s(b), i >> 1) && ok;
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         tc_fence_after();
 #pragma unroll 1
         for (int pass = 0;; ++pass) {
-          // x <- score - reference, -inf behind the last key; mx: the largest
+          // x <- score - reference + kLift, -inf behind the last key; mx: the largest
           float mx = -INFINITY;
           tmem_ld_tile(tmem + kTmemS + b * NH + lane_base, reinterpret_cast<uint32_t(&)[NH / 2]>(x));
           tmem_wait_ld();
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           for (int k = 0; k < NH / 2; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
           if (pass > 0) break;
           // the same decision in all four warps; a row's first tile and a wait that gave up go this way too
-          moved = soft_bar_or(!ok || first || mx > kRise);
+          moved = soft_bar_or(!ok || first || mx > kRise + kLift);
           if (!moved) break;
           if (!first) ok = wait(bar_o, i - 1) && ok;
           if (soft_bar_or(!ok)) {
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             const int col = 8 * j + 2 * (lane & 3);
-            float2 top = first ? make_float2(-INFINITY, -INFINITY) : make_float2(-m[j].x, -m[j].y);
+            float2 top = first ? make_float2(-INFINITY, -INFINITY) : make_float2(kLift - m[j].x, kLift - m[j].y);
 #pragma unroll
             for (int w = 0; w < kSoftWarps; ++w) {
               const float2 e = *reinterpret_cast<const float2*>(exch + w * NH + col);
@@ -668,8 +670,9 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
             }
             if (top.x == -INFINITY) top.x = 0.f;  // no keys
             if (top.y == -INFINITY) top.y = 0.f;
-            const float2 f = first ? make_float2(1.f, 1.f) : make_float2(ex2(-m[j].x - top.x), ex2(-m[j].y - top.y));
-            m[j] = make_float2(-top.x, -top.y);
+            const float2 to = make_float2(kLift - top.x, kLift - top.y);
+            const float2 f = first ? make_float2(1.f, 1.f) : make_float2(ex2(to.x - m[j].x), ex2(to.y - m[j].y));
+            m[j] = to;
             l[j].x *= f.x;
             l[j].y *= f.y;
             if (warp == 0 && lane < 4) *reinterpret_cast<float2*>(s_f + col) = f;

@@ -13,7 +13,10 @@
 namespace dsa {
 
 constexpr int kAttHeader = 256, kAttCounter = 128;  // bytes: start of a workspace, cleared by a launch: status word, row counter
-constexpr float kRise = 8.f;  // log2 of the largest P before the reference moves
+// log2 of the largest weight over the reference's before the reference moves, and
+// of the factor that all weights carry: fp16 holds weights from 2^-24 to below
+// 2^16, so a weight is 0 only below 2^-32 of the reference's.
+constexpr float kRise = 8.f, kLift = 7.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 
 // Status bits of a call: into its workspace's word, which the launch clears, and

@@ -38,8 +38,8 @@
 // queries behind the row's last score (some 7000 cycles a row).
 //
 // Numbers as in dsa_attend.cu: latents exact in fp16, queries fp16 after an
-// exact power of two, P fp16 relative to a reference that the scores pass by
-// 2^8 at most, scores, sums and outputs fp32.
+// exact power of two, P fp16 relative to a reference that the weights pass by
+// 2^8 at most and times 2^7, scores, sums and outputs fp32.
 #include <algorithm>
 
 #include "dsa_attend.cuh"
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     bool ok = true;
     int i = 0;
     for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
-      float c = 0.f, m = 0.f, l = 0.f;  // factor to log2 units, negated reference (from the first tile on), sum
+      float c = 0.f, m = 0.f, l = 0.f;  // factor to log2 units, kLift less the reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         int n_keys = 0;
         if (listed(i)) {
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
         }
         tc_fence_after();
         const uint32_t ts = tmem + kTmemS + 64 * (i & 1);
-        // 32 scores, relative to the reference, -inf behind the last key
+        // 32 scores, relative to the reference, plus kLift, -inf behind the last key
         float x[32];
         auto scores = [&](int q) {
           tmem_ld32(ts + 32 * q, reinterpret_cast<uint32_t(&)[32]>(x));
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
           for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
         }
         // the same decision in both warps of these heads; a wait that gave up goes this way too
-        if (heads_bar_or(bar_id, !ok || first || mx > kRise)) {
+        if (heads_bar_or(bar_id, !ok || first || mx > kRise + kLift)) {
           if (!first) ok = wait(kBarO, i - 1) && ok;
           if (heads_bar_or(bar_id, !ok)) {
             ok = false;
@@ -607,10 +607,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
           *mine = mx - m;
           named_bar_sync(bar_id, 64);
           float top = fmaxf(mx - m, *other);
-          if (!first) top = fmaxf(top, -m);
+          if (!first) top = fmaxf(top, kLift - m);
           if (top == -INFINITY) top = 0.f;  // no keys so far
-          const float f = first ? 1.f : ex2(-m - top);
-          m = -top;
+          const float to = kLift - top, f = first ? 1.f : ex2(to - m);
+          m = to;
           l *= f;
           named_bar_sync(bar_id, 64);
           if (!first) {

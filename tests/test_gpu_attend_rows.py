@@ -165,3 +165,31 @@ def test_workspace_has_the_calls_status_word(T, H):
         assert dsa.dsa_index_device_status(ws) == 2 and int(st) == 2
         dsa.dsa_attend_kv4(scale=SCALE, workspace=ws, status=st, **gpu(x))
         assert dsa.dsa_index_device_status(ws) == 0 and int(st) == 2       # the caller's word collects
+
+
+@pytest.mark.parametrize("T,H,n,drop", [(148, 16, 1 << 20, 25.25), (148, 64, 1 << 18, 22.0), (74, 128, 1 << 20, 25.25), (74, 128, 1 << 19, 25.5)])
+def test_many_small_weights_add_up(T, H, n, drop):
+    # one key at the reference and n - 1 of a weight of 2^-drop each.  Weights are fp16 times 2^7: each is off by at
+    # most 2^-32 (half a subnormal step) or 2^-11 of itself, so the output by at most n 2^-32 |latent| + 2^-11 of the
+    # small keys' part.  The product's fp32 accumulator takes 16 keys a step and may truncate: n / 16 steps of 2^-23
+    # of the output.  The sum takes a thread's two keys (64 of a tile of 128) a step and rounds: n / 64 steps of 2^-24.
+    # exp2 and the quotient: 2^-11 as in serve_ref.check_attend.  The store rounds once, 2^-8.
+    lat = np.concatenate([np.full((1, 512), 1.0), np.full((63, 512), 64.0)])
+    rope = np.zeros((64, 64))
+    rope[1:, 0] = -drop
+    x = dict(entries=ref.kv4_encode(lat, ref.bf16_bits(rope)), page=64)
+    v0, v1 = ref.kv4_decode(x["entries"])[0][:2, 0]       # what the cache holds of 1 and 64
+    q = torch.zeros((T, H, 576), dtype=torch.bfloat16, device="cuda")
+    q[..., 512] = 1.0
+    idx = torch.ones((T, n), dtype=torch.int32, device="cuda")
+    idx[:, 5] = 0
+    pool = torch.from_numpy(x["entries"]).cuda().view(1, 64, 416)
+    zero = torch.zeros(T, dtype=torch.int32, device="cuda")
+    out, lse = dsa.dsa_attend_kv4(q, pool, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), idx, float(np.log(2.0)), row_seq=zero)
+    w = (n - 1) * 2.0 ** -drop
+    want, want_lse = (v0 + v1 * w) / (1.0 + w), np.log1p(w)
+    steps = n / 16 * 2.0 ** -23 + n / 64 * 2.0 ** -24
+    tol = 2.0 ** -8 * want + (1 + 2.0 ** -8) * (n * 2.0 ** -32 * v1 + 2.0 ** -11 * v1 * w + (2.0 ** -11 + steps) * want)
+    assert v1 * w / (1 + w) > 3 * tol                # the small weights would be missed
+    assert float((out.double() - want).abs().max()) <= tol
+    assert float((lse.double() - want_lse).abs().max()) <= n / 64 * 2.0 ** -24 + 2.0 ** -14
