@@ -509,8 +509,9 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  *   row_seq      device, [T] int32: < 0: padding, the row's outputs are left
  *                as they were; >= B: the same, and status bit 1.  NULL: row t
  *                reads sequence t (needs T <= B)
- *   idx          device, [T][n] int32, 1 <= n <= 2^30: out_idx of the index entry
- *                points, or any other list.  An entry at or beyond
+ *   idx          device, [T][n] int32, 1 <= n <= 2^20: out_idx of the index entry
+ *                points, or any other list (a longer one in parts, which lse
+ *                joins).  An entry at or beyond
  *                max_blocks * page_size, or on a page outside [0, n_pages),
  *                is skipped and sets status bit 1
  *   scale        finite
@@ -528,7 +529,8 @@ DSA_API int dsa_kv4_read(const uint8_t* kv_pages, int64_t n_slots, const int32_t
  * largest one of the row (or of its part, where the list is split): 2^-11 of a
  * weight, or 2^-32 of that reference's weight where that is more, so that the
  * small weights of a list move out by at most n 2^-32 max |latent|; lse takes
- * them in fp32.  Results do not depend
+ * them in fp32.  The output sums' additions truncate: at most n / 16 times
+ * 2^-23 of the largest partial sum.  Results do not depend
  * on the rest of the batch's contents.  T == 0 is a no-op.  Requires
  * max_blocks * page_size < 2^31, n_pages * page_size < 2^31, T * H < 2^31.
  */

@@ -813,8 +813,8 @@ def dsa_attend_kv4(q: torch.Tensor, kv_pages: torch.Tensor, block_table: torch.T
 
     q (T, H, 576) bf16 (512 latent, 64 rotary dimensions), kv_pages (n_pages,
     page_size, 416) uint8 (dsa_kv4_write), block_table (B, max_blocks) int32,
-    idx (T, n) int32: positions within the row's sequence (out_idx of the
-    index calls), negative entries skipped.  row_seq (T,) int32 names each
+    idx (T, n) int32, n up to 2^20: positions within the row's sequence (out_idx
+    of the index calls), negative entries skipped.  row_seq (T,) int32 names each
     row's sequence (< 0: padding, left as it was); without it row t reads
     sequence t.  With or without `status`, the status bits of the latest call on
     a workspace are read by dsa_index_device_status(workspace).  Returns (out (T, H, 512) bf16, lse (T, H) fp32).

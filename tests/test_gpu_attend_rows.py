@@ -193,3 +193,18 @@ def test_many_small_weights_add_up(T, H, n, drop):
     assert v1 * w / (1 + w) > 3 * tol                # the small weights would be missed
     assert float((out.double() - want).abs().max()) <= tol
     assert float((lse.double() - want_lse).abs().max()) <= n / 64 * 2.0 ** -24 + 2.0 ** -14
+
+
+@pytest.mark.parametrize("T,H", [(148, 16), (148, 64), (74, 128)])
+def test_equal_weights_on_the_longest_list(T, H):
+    # every key the same, 2^20 of them in one part: the accumulator may truncate at each of the n / 16 steps, 2^-23 of
+    # the output at most; the store rounds once, 2^-8
+    n = 1 << 20
+    e = ref.kv4_encode(np.full((64, 512), 1.0), ref.bf16_bits(np.zeros((64, 64))))
+    v = ref.kv4_decode(e)[0][0, 0]
+    zero = torch.zeros(T, dtype=torch.int32, device="cuda")
+    out, lse = dsa.dsa_attend_kv4(torch.zeros((T, H, 576), dtype=torch.bfloat16, device="cuda"),
+                                  torch.from_numpy(e).cuda().view(1, 64, 416), zero.view(T, 1),
+                                  torch.zeros((T, n), dtype=torch.int32, device="cuda"), 1.0, row_seq=zero)
+    assert float((out.double() - v).abs().max()) <= v * (2.0 ** -8 + n / 16 * 2.0 ** -23)
+    assert float((lse.double() - np.log(n)).abs().max()) <= n / 64 * 2.0 ** -24 + 2.0 ** -18

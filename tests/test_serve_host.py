@@ -93,6 +93,14 @@ def test_attend_refusals():
     assert attend(L, T=0, q=None, idx=None, out=None, ws=None) == 0
 
 
+def test_attend_refuses_lists_longer_than_its_sums_hold():
+    L = dsa.lib()
+    for n in ((1 << 20) + 1, 1 << 22, 1 << 30):
+        assert attend(L, n=n, need=1 << 40) == -1 and b"2^20" in L.dsa_last_error_string()
+        assert L.dsa_attend_kv4_workspace_bytes(2, 16, n) == 0
+    assert L.dsa_attend_kv4_workspace_bytes(2, 16, 1 << 20) > 256
+
+
 def test_binding_refuses_wrong_tensors():
     q = torch.zeros((2, 4, 128), dtype=torch.bfloat16)
     i = torch.zeros(2, dtype=torch.int32)
