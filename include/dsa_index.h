@@ -477,7 +477,9 @@ DSA_API int dsa_index_prepare_fp8(const uint16_t* q, const uint16_t* k, const in
  * pool row slot_map[t]: scale = E4M3(max|x| / 6), code = E2M1(x / scale),
  * both to the nearest with ties to even and saturating, both quotients in
  * fp32 (codes are 0 where the scale is 0: a block's maximum below about
- * 0.006); rotary values are copied.  A block's maximum keeps its precision
+ * 0.006); rotary values are copied.  A NaN among a block's values makes its
+ * scale NaN (0x7F, codes 0), so that the block reads back as NaN; an infinity
+ * is stored as the block's largest value, 2688.  A block's maximum keeps its precision
  * between 0.094 and 2688.  dsa_kv4_read gives rows back in bf16 (exact).
  *   latent    device, [T][512] bf16, 16-byte aligned; rope [T][64] bf16
  *   kv_pages  device, [n_slots][416] bytes, 32-byte aligned: a page pool

@@ -6,7 +6,8 @@
 //   value = code * scale             (6 significant bits: exact in bf16 and fp16)
 //
 // with both quotients in fp32, so the stored bytes are a function of the
-// input alone.  One warp per token, one lane per block: 1152 bytes against
+// input alone.  A NaN makes its block's scale NaN, so the block reads back as
+// NaN; infinities saturate.  One warp per token, one lane per block: 1152 bytes against
 // 416 per token, bound by HBM (and by the launch for a decode step's rows).
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
@@ -25,6 +26,13 @@ constexpr int kKvThreads = 256;
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+}
+
+// The larger of two magnitudes, NaN where either is (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
 
 // Cache entry of row t, or null for padding (slot < 0) and, with the status
@@ -54,12 +62,12 @@ __global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(const Kv4Params p
     for (int i = 0; i < 8; ++i) {
       x[2 * i] = __uint_as_float(u[i] << 16);
       x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+      m = max_nan(m, max_nan(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
     }
     const uint8_t sc = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.f), __NV_SATFINITE, __NV_E4M3);
     const float sv = e4m3_value(sc);
     uint32_t code[2] = {0u, 0u};
-    if (sv > 0.f) {
+    if (sv > 0.f) {  // not where it is 0 or NaN
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t c = __nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(x[2 * i], sv), __fdiv_rn(x[2 * i + 1], sv)),

@@ -88,3 +88,29 @@ def test_offsets_past_32_bits():
     assert np.array_equal(got, ref.kv4_encode(ref.bf16_f64(lat), rope))
     back, _ = dsa.dsa_kv4_read(pool, slot)
     assert np.array_equal(back.double().cpu().numpy(), ref.kv4_decode(got)[0])
+
+
+@pytest.mark.parametrize("T", [1, 9, 2000])
+def test_nan_stays_and_infinity_saturates(T):
+    # a NaN (of either sign, at any place of its block) makes the block NaN and no other; an infinity is the largest value
+    lat, rope = rows(T, 21)
+    rng = np.random.default_rng(T)
+    at = rng.integers(0, 512, T)
+    lat[np.arange(T), at] = np.where(np.arange(T) % 2, 0x7FC0, 0xFF81)
+    inf = (at + 16 * (1 + rng.integers(0, 30, T))) % 512
+    lat[np.arange(T), inf] = np.where(np.arange(T) % 3, 0x7F80, 0xFF80)
+    pool = torch.zeros((T, 1, 416), dtype=torch.uint8, device="cuda")
+    slot = torch.arange(T, dtype=torch.int32, device="cuda")
+    dsa.dsa_kv4_write(bf(lat), bf(rope), pool, slot)
+    x = ref.bf16_f64(lat).reshape(T, 32, 16)
+    nan_block = np.isnan(x).any(-1)
+    fill = np.where(np.isinf(x), np.sign(x) * 1e6, np.where(nan_block[..., None], 0.0, x)).reshape(T, 512)
+    want = ref.kv4_encode(fill, rope)
+    want[:, 256:288][nan_block] = 0x7F
+    got = pool.cpu().numpy().reshape(T, 416)
+    codes = want[:, :256].reshape(T, 32, 8)
+    codes[nan_block] = 0
+    assert np.array_equal(got, want)
+    back, _ = dsa.dsa_kv4_read(pool, slot)
+    assert np.array_equal(back.double().cpu().numpy(), ref.kv4_decode(want)[0], equal_nan=True)
+    assert (torch.isnan(back).reshape(T, 32, 16).all(-1).cpu().numpy() == nan_block).all()
