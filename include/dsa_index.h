@@ -379,6 +379,11 @@ DSA_API int dsa_index_device_status(const void* workspace, uint32_t* status, voi
  *    collect a whole step; without it the same checks skip the same accesses
  *    but go unreported (dsa_attend_kv4 has a workspace, whose status word holds
  *    the bits of its latest call either way).
+ *  - Inputs must be finite, as above.  Bit 3: a query or key that
+ *    dsa_index_prepare* stores or a latent that dsa_kv4_write stores is NaN or
+ *    infinite (rotary bits are copied unseen), or a head's scores made a softmax
+ *    sum of dsa_attend_kv4 NaN or infinite or were all -inf; the outputs of that
+ *    row are unspecified.
  *  - A row with position < 0, slot < 0 or sequence < 0 is padding (the rows
  *    of a captured graph behind the last token): its outputs are left as
  *    they were.

@@ -594,6 +594,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       if (soft_bar_or(!ok || (s_n[i & 1] & kStop))) break;
       const uint32_t item = static_cast<uint32_t>(s_k[i & 1]);
       item_of(it, item, p, g);
+      bool some = false;  // the row (its part) has keys
       float2 c[C], m[C], l[C];  // factor to log2 units, kLift less the reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         const int b = i & 1;
@@ -601,6 +602,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         const int word = s_n[b], n_keys = word & 0xFFFF;
         last = ok && (word & kLast);
         if (first) {
+          some = n_keys > 0;
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             c[j] = *reinterpret_cast<const float2*>(s_c + (n & 1) * NH + 8 * j + 2 * (lane & 3));
@@ -737,6 +739,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
       const int h0 = it.hb * NH;
       if (tid < NH) {  // a head per thread
         const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
+        // NaN or infinite scores; with finite ones the reference's own weight counts
+        if ((!(sum < INFINITY) || (sum == 0.f && some)) && h0 + tid < p.H) report(p, g.err, kErrNonFinite);
         if (g.splits > 1) {
           g.part_ml[static_cast<int64_t>(item) * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_m[tid], sum);
         } else {

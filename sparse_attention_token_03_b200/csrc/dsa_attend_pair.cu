@@ -552,12 +552,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
     bool ok = true;
     int i = 0;
     for (int n = 0; ok && next_item(it, p, g, false); it.k += gridDim.x >> 1, ++n) {
+      bool some = false;  // the row (its part) has keys
       float c = 0.f, m = 0.f, l = 0.f;  // factor to log2 units, kLift less the reference (from the first tile on), sum
       for (bool first = true, last = false; !last; first = false, ++i) {
         int n_keys = 0;
         if (listed(i)) {
           const int meta = s_meta[i % kPairRing];
           last = meta & kLast;
+          some |= (meta & 0xFFFF) > 0;
           n_keys = (meta & 0xFFFF) - part * kHalf;  // of this thread's half
           taken(i);
         } else {
@@ -669,6 +671,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) attend_kv4_pair_kernel(const 
       const int64_t part_row = static_cast<int64_t>(it.k) * 2 * kHalf + rank * kHalf + row;
       const float f = g.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
       if (part == 0 && h < p.H) {
+        // NaN or infinite scores; with finite ones the reference's own weight counts
+        if (!(l < INFINITY) || (l == 0.f && some)) report(p, g.err, kErrNonFinite);
         if (g.splits > 1)
           g.part_ml[part_row] = make_float2(l == 0.f ? -INFINITY : -m, l);
         else if (p.lse)

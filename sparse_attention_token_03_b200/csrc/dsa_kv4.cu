@@ -28,13 +28,6 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
 
-// The larger of two magnitudes, NaN where either is (fmaxf drops it).
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-
 // Cache entry of row t, or null for padding (slot < 0) and, with the status
 // bit set, for a slot outside the pool.
 __device__ __forceinline__ uint8_t* entry_of(const Kv4Params& p, int64_t t, int lane) {
@@ -64,6 +57,7 @@ __global__ void __launch_bounds__(kKvThreads) kv4_write_kernel(const Kv4Params p
       x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
       m = max_nan(m, max_nan(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
     }
+    if (p.status && !(m < INFINITY)) atomicOr(p.status, kErrNonFinite);
     const uint8_t sc = __nv_cvt_float_to_fp8(__fdiv_rn(m, 6.f), __NV_SATFINITE, __NV_E4M3);
     const float sv = e4m3_value(sc);
     uint32_t code[2] = {0u, 0u};

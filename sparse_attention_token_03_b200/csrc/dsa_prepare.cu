@@ -35,6 +35,9 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = kPrepThreads / 8;  // rows in flight per step
 constexpr int kW = 128;                      // row width
 
+__device__ __forceinline__ void non_finite(uint32_t* status, int64_t row) {
+  if (row >= 0 && status) atomicOr(status, kErrNonFinite);
+}
 __device__ __forceinline__ float sum8(float v) {
 #pragma unroll
   for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o, 8);
@@ -42,7 +45,7 @@ __device__ __forceinline__ float sum8(float v) {
 }
 __device__ __forceinline__ float max8(float v) {
 #pragma unroll
-  for (int o = 4; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o, 8));
+  for (int o = 4; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(~0u, v, o, 8));
   return v;
 }
 
@@ -82,12 +85,20 @@ __device__ __forceinline__ RawRow load_row(const uint16_t* rows, int64_t row, Ch
 }
 
 // Norm, rotation (rotate: this lane holds pairs, cs their angles) and store of
-// one row; nothing is stored for row < 0.  All 32 lanes of the warp call it.
+// one row; nothing is stored for row < 0.  A stored row with a NaN or an
+// infinity is reported.  All 32 lanes of the warp call it.
 template <bool FP8, bool INTER>
 __device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n, float eps, bool rotate,
-                                           const float2 (&cs)[8], Chunks c, void* out, float* scale, int64_t row, int l) {
+                                           const float2 (&cs)[8], Chunks c, void* out, float* scale, int64_t row, int l,
+                                           uint32_t* status) {
   float x[16];
   const uint32_t u[8] = {raw.a.x, raw.a.y, raw.a.z, raw.a.w, raw.b.x, raw.b.y, raw.b.z, raw.b.w};
+  if (!FP8 && n.norm == kNormNone) {
+    uint32_t top = 0;  // the largest magnitudes' bits, two values a word
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, u[i] & 0x7FFF7FFFu);
+    if ((top & 0xFFFFu) >= 0x7F80u || top >= 0x7F800000u) non_finite(status, row);
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
@@ -105,7 +116,9 @@ __device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n,
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) s = fmaf(x[i], x[i], s);
-    const float inv = rsqrtf(fmaf(sum8(s), 1.f / kW, eps));
+    const float v = fmaf(sum8(s), 1.f / kW, eps);
+    if (!FP8 && !(v < INFINITY)) non_finite(status, row);
+    const float inv = rsqrtf(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * n.w[i];
     if (n.bias) {
@@ -128,8 +141,9 @@ __device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n,
   if constexpr (FP8) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+    for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(x[i]));
     m = max8(m);
+    if (!(m < INFINITY)) non_finite(status, row);
     // a row of zeros has scale 1; a scale is never subnormal, so that its
     // reciprocal is finite
     const float sc = m > 0.f ? fmaxf(__fdiv_rn(m, 448.f), 1.17549435e-38f) : 1.f;
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
       if (l == 0 && p.status) atomicOr(p.status, kErrOverflow);
       slot = -1;
     }
-    finish_row<FP8, INTER>(rawk, n, p.eps, rotate, cs, c, p.k_out, p.k_scale, slot, l);
+    finish_row<FP8, INTER>(rawk, n, p.eps, rotate, cs, c, p.k_out, p.k_scale, slot, l, p.status);
   }
   load_norm(n, p.q_norm, p.q_weight, p.q_bias, c);
 #pragma unroll 1
@@ -243,7 +257,8 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
       for (int i = 0; i < U; ++i) {
         const int h = h0 + i * kPrepRows + hw;
         if (h0 + i * kPrepRows + (hw & ~3) < h_hi)  // warp-uniform
-          finish_row<FP8, INTER>(now[i], n, p.eps, rotate, cs, c, p.q_out, p.q_scale, h < h_hi ? (t0 + g) * p.H + h : -1, l);
+          finish_row<FP8, INTER>(now[i], n, p.eps, rotate, cs, c, p.q_out, p.q_scale, h < h_hi ? (t0 + g) * p.H + h : -1, l,
+                                  p.status);
       }
     }
     g = g1;

@@ -42,6 +42,13 @@ inline PageDiv page_div(int d) {
   return {static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), 31 + s};
 }
 
+// The larger of two magnitudes, NaN where either is (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 struct TablesParams {
   const int32_t* cached_len;  // [B]
   const int32_t* new_len;     // [B]
