@@ -381,7 +381,7 @@ DSA_API int dsa_index_device_status(const void* workspace, uint32_t* status, voi
  *    the bits of its latest call either way).
  *  - Inputs must be finite, as above.  Bit 3: a query or key that
  *    dsa_index_prepare* stores or a latent that dsa_kv4_write stores is NaN or
- *    infinite (rotary bits are copied unseen), or a head's scores made a softmax
+ *    infinite, or passes a norm's range (rotary bits are copied unseen), or a head's scores made a softmax
  *    sum of dsa_attend_kv4 NaN or infinite or were all -inf; the outputs of that
  *    row are unspecified.
  *  - A row with position < 0, slot < 0 or sequence < 0 is padding (the rows
@@ -437,7 +437,9 @@ DSA_API int dsa_block_tables(const int32_t* cached_len, const int32_t* new_len, 
  * pair is dimensions (2i, 2i + 1) when `interleaved`, else (i, i + rot / 2).
  * Queries and keys have norms of their own.  Statistics and rotation are
  * fp32, the angle is reduced in fp64 (exact to fp32 at any position); the
- * store rounds once.
+ * store rounds once.  The mean under a norm's root plus eps must lie in [2^-100,
+ * 2^120): a row outside (magnitudes above some 2^59, or below 2^-49 with an eps
+ * below 2^-100) is unspecified and sets status bit 3.
  *   q         device, [T][H][128] bf16 (1 <= H <= 256)
  *   k         device, [T][128] bf16
  *   position  device, [T] int32; < 0: padding, neither row is written

@@ -35,6 +35,10 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepRows = kPrepThreads / 8;  // rows in flight per step
 constexpr int kW = 128;                      // row width
 
+// A norm's mean square plus eps below which its squares have lost digits, and
+// above which their sum may be infinite; a NaN is neither.  (Such rows scaled
+// first, out of the walk's way, cost ordinary ones 20%: 134 us for 110.)
+constexpr float kNormLow = 7.8886091e-31f, kNormHigh = 1.3292280e36f;  // 2^-100, 2^120
 __device__ __forceinline__ void non_finite(uint32_t* status, int64_t row) {
   if (row >= 0 && status) atomicOr(status, kErrNonFinite);
 }
@@ -117,7 +121,7 @@ __device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n,
 #pragma unroll
     for (int i = 0; i < 16; ++i) s = fmaf(x[i], x[i], s);
     const float v = fmaf(sum8(s), 1.f / kW, eps);
-    if (!FP8 && !(v < INFINITY)) non_finite(status, row);
+    if (!(v >= kNormLow && v < kNormHigh)) non_finite(status, row);
     const float inv = rsqrtf(v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = x[i] * inv * n.w[i];

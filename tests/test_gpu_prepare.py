@@ -193,6 +193,55 @@ def test_prepare_many_tokens_in_place():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H", [(40, 5), (320, 33), (1300, 4)])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 1e-30])
+def test_prepare_norms_over_their_range(norm, eps, T, H, fp8):
+    # magnitudes over the whole range of a norm; then single rows beyond it, which are flagged and change no other
+    rng = np.random.default_rng(T)
+    x = make(T, H, 64, norm, norm, seed=T)
+    size = 2.0 ** rng.integers(-46, 56, (T, H + 1))
+    x["q"] = ref.bf16_bits(ref.bf16_f64(x["q"]) * size[:, :H, None])
+    x["k"] = ref.bf16_bits(ref.bf16_f64(x["k"]) * size[:, H:])
+
+    def run(x):
+        a = [gpu(x[k]) for k in ("q", "k", "pos", "inv_freq")]
+        kw = dict(slot_map=gpu(x["slot"]), eps=eps, q_norm=norm, k_norm=norm, status=torch.zeros(1, dtype=torch.int32, device="cuda"),
+                  **{k: gpu(x[k]) for k in ("q_weight", "q_bias", "k_weight", "k_bias")})
+        if fp8:
+            k_out, ks = torch.zeros((x["n"], 128), dtype=torch.uint8, device="cuda"), torch.zeros(x["n"], device="cuda")
+            r = [t.cpu().numpy() for t in dsa.dsa_index_prepare_fp8(*a, k_out, ks, **kw)]
+            return (r[0], r[2][x["slot"]], r[1], r[3][x["slot"]]), int(kw["status"])
+        k_out = torch.zeros((x["n"], 128), dtype=torch.bfloat16, device="cuda")
+        q, k = dsa.dsa_index_prepare(*a, k_out, **kw)
+        return (q.double().cpu().numpy(), k.double().cpu().numpy()[x["slot"]]), int(kw["status"])
+
+    good, st = run(x)
+    assert st == 0
+    raw_q, raw_k = ref.bf16_f64(x["q"]), ref.bf16_f64(x["k"])
+    yq = ref.norm_rotate(raw_q, x["pos"], x["inv_freq"], norm, x["q_weight"], x["q_bias"], eps, False)
+    yk = ref.norm_rotate(raw_k[:, None], x["pos"], x["inv_freq"], norm, x["k_weight"], x["k_bias"], eps, False)[:, 0]
+    # bound() sees the rows at a size where its own floor of the deviation does not count
+    unit = lambda r: r / np.abs(r).max(-1, keepdims=True)
+    for i, (raw, y, name) in enumerate(((unit(raw_q), yq, "q"), (unit(raw_k), yk, "k"))):
+        if fp8:
+            check_fp8(good[i], good[2 + i], raw, y, norm, name)
+        else:
+            check_bf16(good[i], raw, y, norm, name)
+    for e in (62, 100, 120) + ((-54, -90, -125) if eps == 0 else ()):
+        for name, at in (("q", (T // 2, H - 1)), ("k", (T - 1,))):
+            y = dict(x, **{name: x[name].copy()})
+            row = rng.standard_normal(128)
+            y[name][at] = ref.bf16_bits(row / np.sqrt((row * row).mean()) * 2.0 ** e)
+            got, st = run(y)
+            assert st == 8, (e, name)
+            for i, (g, w) in enumerate(zip(got, good)):
+                if "qk"[i % 2] == name:
+                    g[at] = w[at]
+                assert np.array_equal(g, w)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T,H,rot,norms", [(297, 33, 64, 0), (301, 64, 32, 1), (741, 5, 128, 2), (999, 40, 64, 1)])
 def test_prepare_tokens_in_small_groups(T, H, rot, norms, fp8):
     test_prepare(T, H, rot, norms, False, fp8)
