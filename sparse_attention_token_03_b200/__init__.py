@@ -8,7 +8,8 @@ computation runs in the library's CUDA kernels; there is no fallback.
 
 The serving calls, whose kernels take a few microseconds in a decode step, have
 a native host side (serve_binding.cpp, _serve_binding.so) that does the same
-for the common case in one call.
+for the common case in one call.  It is loaded by the first of them; no other
+call needs it.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import warnings
 from pathlib import Path
 
 import torch
@@ -127,14 +129,18 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
         L.dsa_profile_enable.restype = I
         L.dsa_profile_read.argtypes = [P, P, I, P]
         L.dsa_profile_read.restype = I
-        _load_binding(L, build_if_missing)
         _lib = L
     return _lib
 
 
-def _load_binding(L: ctypes.CDLL, build_if_missing: bool):
-    global _serve
-    if build_if_missing and _build.binding_stale():
+class _NoBinding:
+    """Stands in for serve_binding.cpp where it cannot be had: every call goes on to the Python checks."""
+
+    kv4_write = kv4_read = block_tables = prepare = attend = staticmethod(lambda *a: None)
+
+
+def _load_binding(L: ctypes.CDLL):
+    if _build.binding_stale():
         _build.build_binding()
     loader = importlib.machinery.ExtensionFileLoader("_serve_binding", str(_build.BINDING))
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve_binding", loader))
@@ -142,14 +148,23 @@ def _load_binding(L: ctypes.CDLL, build_if_missing: bool):
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.dsa_block_tables, L.dsa_index_prepare, L.dsa_index_prepare_fp8, L.dsa_kv4_write, L.dsa_kv4_read,
         L.dsa_attend_kv4, L.dsa_attend_kv4_workspace_bytes)))
-    _serve = module
+    return module
 
 
 def _native():
     """serve_binding.cpp: the common case of the serving calls.  It returns None
-    where an argument is anything else, and the caller goes on to its own checks."""
+    where an argument is anything else, and the caller goes on to its own checks.
+    Only the serving calls load it, and they do without it where there is no compiler
+    or no torch to build it against."""
+    global _serve
     if _serve is None:
-        lib()
+        L = lib()
+        try:
+            _serve = _load_binding(L)
+        except Exception as e:
+            warnings.warn(f"the native host side of the serving calls is not available ({e}); their Python checks "
+                          "take over, some 10 to 25 us a call", RuntimeWarning, stacklevel=3)
+            _serve = _NoBinding
     return _serve
 
 

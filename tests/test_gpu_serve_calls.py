@@ -94,3 +94,29 @@ def test_the_librarys_errors():
         dsa.dsa_kv4_write(x["latent"].t().contiguous().t(), x["rope"], kv, x["slot"])
     with pytest.raises(TypeError):
         dsa.dsa_kv4_read(kv, x["slot"].long())
+
+
+def test_python_checks_alone_give_the_same(monkeypatch):
+    # every serving call with the native host side and, as where it cannot be built, without it
+    x = tokens(70)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    seq, q_att = torch.zeros(70, dtype=torch.int32, device="cuda"), torch.randn((70, 40, 576), device="cuda").bfloat16()
+
+    def step():
+        table = i(3, -1, -1).view(1, 3)
+        out = list(dsa.dsa_block_tables(i(20), i(70), table, i(0, 1, 2), i(0), 4, 64, 75)) + [table]
+        slot = out[0][:70].contiguous()
+        pool = torch.zeros((4, 64, 128), dtype=torch.bfloat16, device="cuda")
+        out += dsa.dsa_index_prepare(x["q"], x["k"], x["position"], x["inv_freq"], pool, slot_map=slot, k_norm="rms", k_weight=x["w"])
+        k8, ks = torch.zeros((4, 64, 128), dtype=torch.uint8, device="cuda"), torch.zeros((4, 64), device="cuda")
+        out += dsa.dsa_index_prepare_fp8(x["q"], x["k"], x["position"], x["inv_freq"], k8, ks, slot_map=slot, interleaved=True)
+        kv = dsa.dsa_kv4_write(x["latent"], x["rope"], torch.zeros((4, 64, 416), dtype=torch.uint8, device="cuda"), slot)
+        out += [kv, *dsa.dsa_kv4_read(kv, slot)]
+        idx = torch.arange(20, 90, dtype=torch.int32, device="cuda").repeat(70, 1)
+        return out + list(dsa.dsa_attend_kv4(q_att, kv, table, idx, 0.1, row_seq=seq))
+
+    a = step()
+    assert dsa._serve is not dsa._NoBinding
+    monkeypatch.setattr(dsa, "_serve", dsa._NoBinding)
+    b = step()
+    assert len(a) == len(b) and all(torch.equal(u, v) for u, v in zip(a, b))

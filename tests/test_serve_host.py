@@ -2,6 +2,9 @@
 and the 64-bit references' own pins."""
 
 import ctypes
+import subprocess
+import sys
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -117,6 +120,34 @@ def test_binding_refuses_wrong_tensors():
         dsa.dsa_attend_kv4(q, torch.zeros((2, 64, 416), dtype=torch.int8), i, i, 1.0)
     with pytest.raises(TypeError):
         dsa.dsa_block_tables(i.long(), i, i.view(2, 1), i, i[:1], 4, 64, 8)
+
+
+def test_library_does_not_need_the_native_host_side():
+    # no object, no compiler: the index calls load as they are, the serving calls warn once and check in Python
+    code = """
+import os, warnings
+from pathlib import Path
+os.environ["CXX"] = "/bin/false"
+import torch
+import sparse_attention_token_03_b200 as dsa
+from sparse_attention_token_03_b200 import build
+build.BINDING = Path("/nonexistent/none.so")
+with warnings.catch_warnings():
+    warnings.simplefilter("error")
+    assert dsa.dsa_index_prefill_workspace_bytes(4, 4, 64, 128, 8) > 0
+    assert dsa.lib(build_if_missing=False) is dsa.lib()
+slots = torch.zeros(2, dtype=torch.int32)
+for i in range(2):
+    with warnings.catch_warnings(record=True) as seen:
+        warnings.simplefilter("always")
+        try:
+            dsa.dsa_kv4_read(torch.zeros((2, 64, 416), dtype=torch.uint8), slots)
+            raise SystemExit("accepted a CPU tensor")
+        except ValueError as e:
+            assert "CUDA" in str(e)
+    assert [w.category for w in seen] == ([RuntimeWarning] if i == 0 else []), seen
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=Path(__file__).resolve().parent.parent, timeout=300)
 
 
 def test_reference_formats():
