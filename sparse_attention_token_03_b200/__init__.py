@@ -7,7 +7,7 @@ pointers plus the current CUDA stream to the C ABI.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback.
 
 The serving calls, whose kernels take a few microseconds in a decode step, have
-a native host side (serve_binding.cpp, _serve_binding.so) that does the same
+a native host side (serve_binding.cpp, _serve_binding-*.so) that does the same
 for the common case in one call.  It is loaded by the first of them; no other
 call needs it.
 """

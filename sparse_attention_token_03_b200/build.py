@@ -1,8 +1,9 @@
 """Build libdsa_index.so in-tree with nvcc for sm_100a (no torch JIT cache), and
-_serve_binding.so, the native host side of the serving calls, with g++."""
+_serve_binding-*.so, the native host side of the serving calls, with g++."""
 
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -14,7 +15,21 @@ CSRC = PKG / "csrc"
 INCLUDE = PKG.parent / "include"
 LIB = PKG / "libdsa_index.so"
 BINDING_SRC = PKG / "serve_binding.cpp"
-BINDING = PKG / "_serve_binding.so"
+
+
+def binding_path(torch_version: str, python_tag: str) -> Path:
+    """The object inlines torch's C++ layouts and CPython's API: one per version of both."""
+    return PKG / f"_serve_binding-{python_tag}-torch{torch_version}.so"
+
+
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # the library itself builds without it
+        return "-none"
+
+
+BINDING = binding_path(_torch_version(), sys.implementation.cache_tag)
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -150,6 +150,20 @@ for i in range(2):
     subprocess.run([sys.executable, "-c", code], check=True, cwd=Path(__file__).resolve().parent.parent, timeout=300)
 
 
+def test_native_host_side_is_built_for_one_torch_and_python(tmp_path, monkeypatch):
+    from sparse_attention_token_03_b200 import build
+    tag = sys.implementation.cache_tag
+    assert build.BINDING == build.binding_path(torch.__version__, tag)
+    # an object of another torch or Python is another file: it is neither loaded nor taken for this one's
+    other = [build.binding_path(torch.__version__, "cpython-399"), build.binding_path("9.9.9", tag)]
+    assert len({build.BINDING, *other}) == 3
+    monkeypatch.setattr(build, "PKG", tmp_path)
+    for p in other:
+        (tmp_path / p.name).write_bytes(b"")
+    monkeypatch.setattr(build, "BINDING", build.binding_path(torch.__version__, tag))
+    assert build.binding_stale()
+
+
 def test_reference_formats():
     # E4M3 against torch's own conversion; E2M1 rounding at its midpoints (ties to the even code)
     t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy().astype(np.float64)
