@@ -4,7 +4,7 @@
 //   z(t,h,j) = scale * (q(t,h) . [latent_j, rotary_j])
 //   out(t,h) = sum_j softmax_j(z) latent_j,   lse(t,h) = log sum_j exp z
 //
-// A block works on one row, up to 64 heads and a range of the row's list, in
+// A block works on one row, all its heads (up to 64) and a range of its list, in
 // tiles of 64 keys (dsa_attend_pair.cu has the kernel for more heads).  Both
 // products have the keys' or the latent dimensions as the MMA's rows and the
 // heads as its columns,
@@ -13,8 +13,8 @@
 //   O^T [512 x heads]     += V^T [512 x 64] P^T       (M = 128, 4 x 4 K steps)
 //
 // so that O^T of 64 heads takes 256 of the 512 TMEM columns (heads as rows
-// would fill all of them with O alone) and 8 or 16 heads cost no more than
-// their columns.  K and V are the same decoded tile: 64-dimension column
+// would fill all of them with O alone) and few heads cost their columns, in
+// blocks of 16, 32 or 64.  K and V are the same decoded tile: 64-dimension column
 // blocks of [64 keys][128 bytes] with the 128-byte swizzle, read K-major for
 // S and M-major for O.
 //
@@ -110,14 +110,14 @@ struct AttSmem {
 };
 static_assert(AttSmem<64>::bytes <= 227u * 1024u && AttSmem<32>::bytes <= 227u * 1024u, "shared memory budget");
 
-// One row, head block and list range of the grid.
+// An item is one row and list range.
 struct AttGrid {
-  int head_blocks, splits, tiles;  // tiles: of a whole list
-  uint32_t items;                  // T * head_blocks * splits, below 2^31
-  uint32_t* next;                  // null (block b takes items b, b + grid, ...) or a counter at 0 of the items behind
-                                   // the blocks' first ones that are taken
-  float4* part_o;                  // [T][head_blocks][splits] blocks of NH x 512 in the order of part_index
-  float2* part_ml;                 // [T][head_blocks][splits][NH]
+  int splits, tiles;               // tiles: of a whole list
+  uint32_t items;                  // T * splits, below 2^31
+  uint32_t* next;                  // null (one item a block) or a counter at 0 of the items behind the blocks' first
+                                   // ones that are taken
+  float4* part_o;                  // [T][splits] blocks of NH x 512 in the order of part_index
+  float2* part_ml;                 // [T][splits][NH]
   uint32_t* err;                   // the workspace's status word
   PageDiv div;
 };
@@ -199,12 +199,12 @@ __device__ __forceinline__ constexpr int dim_of(int s, int p) { return 256 * (s 
 // Query rows r0, r0 + step, ... to shared memory as the MMA reads them (see the
 // file's comment), two rows in flight.
 template <int NH>
-__device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, int h0, uint8_t* q_buf, float* s_c, int r0,
+__device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, uint8_t* q_buf, float* s_c, int r0,
                                               int step, int lane) {
-  auto live = [&](int r) { return r < NH && h0 + r < p.H; };
+  auto live = [&](int r) { return r < NH && r < p.H; };
   uint4 v[2][3];
-  load_query_row(v[0], p, t, h0 + r0, live(r0), lane);
-  load_query_row(v[1], p, t, h0 + r0 + step, live(r0 + step), lane);
+  load_query_row(v[0], p, t, r0, live(r0), lane);
+  load_query_row(v[1], p, t, r0 + step, live(r0 + step), lane);
 #pragma unroll 1
   for (int r = r0; r < NH; r += step) {
     uint4 now[3];
@@ -213,21 +213,21 @@ __device__ __forceinline__ void stage_queries(const AttendParams& p, int64_t t, 
       now[k] = v[0][k];
       v[0][k] = v[1][k];
     }
-    load_query_row(v[1], p, t, h0 + r + 2 * step, live(r + 2 * step), lane);
+    load_query_row(v[1], p, t, r + 2 * step, live(r + 2 * step), lane);
     store_query_row(now, p.scale, q_buf, AttSmem<NH>::q_block, r, s_c, lane, part_of);
   }
 }
 
 // The same rows for a whole number of pairs, two at once.
 template <int NH>
-__device__ __forceinline__ void stage_query_pairs(const AttendParams& p, int64_t t, int h0, uint8_t* q_buf, float* s_c,
+__device__ __forceinline__ void stage_query_pairs(const AttendParams& p, int64_t t, uint8_t* q_buf, float* s_c,
                                                   int r0, int step, int lane) {
-  auto live = [&](int r) { return h0 + r < p.H; };
+  auto live = [&](int r) { return r < p.H; };
 #pragma unroll 1
   for (int r = r0; r < NH; r += 2 * step) {
     uint4 v[2][3];
-    load_query_row(v[0], p, t, h0 + r, live(r), lane);
-    load_query_row(v[1], p, t, h0 + r + step, live(r + step), lane);
+    load_query_row(v[0], p, t, r, live(r), lane);
+    load_query_row(v[1], p, t, r + step, live(r + step), lane);
     const int two[2] = {r, r + step};
     store_query_rows<2>(v, p.scale, q_buf, AttSmem<NH>::q_block, two, s_c, lane, part_of);
   }
@@ -236,13 +236,12 @@ __device__ __forceinline__ void stage_query_pairs(const AttendParams& p, int64_t
 // What item k stands for; false for padding and a sequence that does not exist.
 struct AttItem {
   int64_t t;
-  int hb, split, seq;
+  int split, seq;
 };
 __device__ __forceinline__ bool item_of(AttItem& it, uint32_t k, const AttendParams& p, const AttGrid& g) {
   const uint32_t row = k / static_cast<uint32_t>(g.splits);
   it.split = static_cast<int>(k - row * g.splits);
-  it.t = row / static_cast<uint32_t>(g.head_blocks);
-  it.hb = static_cast<int>(row - static_cast<uint32_t>(it.t) * g.head_blocks);
+  it.t = row;
   it.seq = p.row_seq ? __ldg(p.row_seq + it.t) : static_cast<int>(it.t);
   return it.seq >= 0 && it.seq < p.B;
 }
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
   // the queries of the block's first item by all warps but the issuing ones and the list's
   if (warp < kMmaWarp) {
     if (first_ok) {
-      stage_queries<NH>(p, it.t, it.hb * NH, smem, s_c, warp, kMmaWarp, lane);
+      stage_queries<NH>(p, it.t, smem, s_c, warp, kMmaWarp, lane);
       fence_proxy_async_smem();
     }
     named_bar_sync(2, kWorkThreads);
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           if (lane == 0) k = gridDim.x + atomicAdd(g.next, 1u);
           k = __shfl_sync(~0u, k, 0);
         } else {
-          k += gridDim.x;
+          k = g.items;
         }
       };
       for (int n = 0; ok && k < g.items; advance()) {
@@ -556,18 +555,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         ++n;
         const int q = L::q_bufs == 2 ? n & 1 : 0;
         // on their way to L2 during the wait
-        const char* src = reinterpret_cast<const char*>(p.q + (it.t * p.H + it.hb * NH) * kKvQ);
-        const int bytes = min(NH, p.H - it.hb * NH) * 2 * kKvQ;
+        const char* src = reinterpret_cast<const char*>(p.q + it.t * p.H * kKvQ);
+        const int bytes = p.H * 2 * kKvQ;
         for (int at = (tid - kSoftThreads) * 128; at < bytes; at += kLoadWarps * 32 * 128)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(src + at));
         ok = wait(bar_q_free(q), (L::q_bufs == 2 ? n >> 1 : n) + 1) && wait(bar_c_free(n), (n >> 1) + 1);
         if (!ok) break;
         if constexpr (NH >= 2 * kLoadWarps)
-          stage_query_pairs<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps,
-                                kLoadWarps, lane);
+          stage_query_pairs<NH>(p, it.t, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps, lane);
         else
-          stage_queries<NH>(p, it.t, it.hb * NH, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps,
-                            lane);
+          stage_queries<NH>(p, it.t, smem + q * L::q_bytes, s_c + (n & 1) * NH, warp - kSoftWarps, kLoadWarps, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q(q));
@@ -736,17 +733,16 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
         }
       }
       named_bar_sync(1, kSoftThreads);
-      const int h0 = it.hb * NH;
       if (tid < NH) {  // a head per thread
         const float sum = (exch[tid] + exch[NH + tid]) + (exch[2 * NH + tid] + exch[3 * NH + tid]);
         // NaN or infinite scores; with finite ones the reference's own weight counts
-        if ((!(sum < INFINITY) || (sum == 0.f && some)) && h0 + tid < p.H) report(p, g.err, kErrNonFinite);
+        if ((!(sum < INFINITY) || (sum == 0.f && some)) && tid < p.H) report(p, g.err, kErrNonFinite);
         if (g.splits > 1) {
           g.part_ml[static_cast<int64_t>(item) * NH + tid] = make_float2(sum == 0.f ? -INFINITY : s_m[tid], sum);
         } else {
           s_f[tid] = sum == 0.f ? 0.f : 1.f / sum;
-          if (p.lse && h0 + tid < p.H)
-            p.lse[it.t * p.H + h0 + tid] = sum == 0.f ? -INFINITY : (s_m[tid] + log2f(sum)) * kLn2;
+          if (p.lse && tid < p.H)
+            p.lse[it.t * p.H + tid] = sum == 0.f ? -INFINITY : (s_m[tid] + log2f(sum)) * kLn2;
         }
       }
       named_bar_sync(1, kSoftThreads);
@@ -770,7 +766,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
           tmem_ld16(tmem + kTmemO + lane_base + q, o);
           tmem_wait_ld();
           const int dim = (dim_of(s, warp) + lane) & ~1;
-          uint16_t* dst = p.out + (it.t * p.H + h0 + h + (lane & 1)) * kKvLat + dim;
+          uint16_t* dst = p.out + (it.t * p.H + h + (lane & 1)) * kKvLat + dim;
           // lanes pair up: the even one stores two dimensions of a head, the odd one of the next head
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -778,7 +774,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attend_kv4_kernel(const Attend
             const float a = __uint_as_float(o[k]) * f.x, d = __uint_as_float(o[k + 1]) * f.y;
             const float other = __shfl_xor_sync(~0u, lane & 1 ? a : d, 1);
             const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(other, d) : __floats2bfloat162_rn(a, other);
-            if (h0 + h + k + (lane & 1) < p.H) *reinterpret_cast<__nv_bfloat162*>(dst + k * kKvLat) = v;
+            if (h + k + (lane & 1) < p.H) *reinterpret_cast<__nv_bfloat162*>(dst + k * kKvLat) = v;
           }
           __syncwarp();
         }
@@ -801,14 +797,12 @@ template <int NH>
 __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, const AttGrid g) {
   __shared__ __align__(16) uint16_t s_o[8][128 + 8];
   const int s = blockIdx.x % kParts, j = blockIdx.x / kParts % (NH / 8);
-  const int64_t row = blockIdx.x / (kParts * (NH / 8));
-  const int hb = static_cast<int>(row % g.head_blocks);
-  const int64_t t = row / g.head_blocks;
+  const int64_t t = blockIdx.x / (kParts * (NH / 8));
   const int seq = p.row_seq ? __ldg(p.row_seq + t) : static_cast<int>(t);
-  const int h0 = hb * NH + 8 * j;
+  const int h0 = 8 * j;
   if (seq < 0 || seq >= p.B || h0 >= p.H) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, pq = warp & 3, half = warp >> 2;
-  const int64_t item0 = row * g.splits;
+  const int64_t item0 = t * g.splits;
   const float4* ml = reinterpret_cast<const float4*>(g.part_ml + item0 * NH + 8 * j + 2 * (lane & 3));  // two heads
   constexpr int kMl = NH / 2;                                 // float4 between splits
   constexpr int64_t kO = int64_t(NH) * kKvLat / 4;
@@ -855,24 +849,22 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, 
 }
 
 struct AttPlan {
-  int NH, head_blocks, splits, tiles;
+  int NH, splits, tiles;
   size_t off_ml, off_o, bytes;
 };
 
 AttPlan plan_attend(int64_t T, int H, int n, int sms) {
   AttPlan P{};
   P.NH = H <= 16 ? 16 : H <= 32 ? 32 : 64;
-  P.head_blocks = (H + P.NH - 1) / P.NH;
   P.tiles = (n + kKt - 1) / kKt;
-  const int64_t items = T * P.head_blocks;
   // fewer rows than SMs: parts of at least two tiles (one row of 64 heads and 2048 entries: 21.6 us in 16 parts,
   // 25 us in 32 of one tile, whose partial outputs cost more than their tile)
-  P.splits = items >= sms || items == 0 ? 1 : static_cast<int>(std::min<int64_t>(sms / items, (P.tiles + 1) / 2));
+  P.splits = T >= sms || T == 0 ? 1 : static_cast<int>(std::min<int64_t>(sms / T, (P.tiles + 1) / 2));
   P.off_ml = kAttHeader;
   P.off_o = P.off_ml;
   P.bytes = kAttHeader;
   if (P.splits > 1) {
-    const size_t rows = static_cast<size_t>(items) * P.splits * P.NH;
+    const size_t rows = static_cast<size_t>(T) * P.splits * P.NH;
     P.off_o = (P.off_ml + rows * sizeof(float2) + 255) / 256 * 256;
     P.bytes = P.off_o + rows * kKvLat * sizeof(float);
   }
@@ -888,7 +880,7 @@ cudaError_t launch_nh(const AttendParams& p, const AttGrid& g, int sms, cudaStre
   attend_kv4_kernel<NH><<<std::min(g.items, static_cast<uint32_t>(std::max(sms, 1))), kAttThreads, bytes, st>>>(p, g);
   e = cudaGetLastError();
   if (e != cudaSuccess || g.splits == 1) return e;
-  attend_join_kernel<NH><<<static_cast<unsigned>(p.T * g.head_blocks * kParts * (NH / 8)), 256, 0, st>>>(p, g);
+  attend_join_kernel<NH><<<static_cast<unsigned>(p.T * kParts * (NH / 8)), 256, 0, st>>>(p, g);
   return cudaGetLastError();
 }
 
@@ -902,7 +894,7 @@ cudaError_t launch_attend_kv4(const AttendParams& p, void* workspace, int sms, c
   if (p.H > 64) return launch_attend_kv4_pair(p, workspace, sms, st);
   const AttPlan P = plan_attend(p.T, p.H, p.n, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttGrid g{P.head_blocks, P.splits, P.tiles, static_cast<uint32_t>(p.T * P.head_blocks * P.splits), nullptr,
+  AttGrid g{P.splits, P.tiles, static_cast<uint32_t>(p.T * P.splits), nullptr,
             reinterpret_cast<float4*>(ws + P.off_o),
             reinterpret_cast<float2*>(ws + P.off_ml), reinterpret_cast<uint32_t*>(ws), page_div(p.page_size)};
   // lists of unequal lengths: blocks take rows as they get free (501 rows of 16 heads and up to 1023 entries: 81 us,

@@ -186,9 +186,8 @@ __device__ __forceinline__ void finish_row(const RawRow& raw, const NormLane& n,
 
 // A block takes G consecutive tokens, or with G = 1 also just 32 of a token's
 // heads (blockIdx.y): it forms the tokens' angles with all threads, then each
-// group of 8 lanes walks the rows on its own, U rows of a token at a time with the
-// next U in flight.
-template <bool FP8, bool INTER, int G, int U>
+// group of 8 lanes walks the rows on its own, the next row in flight.
+template <bool FP8, bool INTER, int G>
 __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_kernel(const PrepareParams p) {
   __shared__ float2 s_cs[G][kW / 2];
   __shared__ int s_pos[G];
@@ -197,15 +196,11 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
   const int h_lo = G > 1 ? 0 : blockIdx.y * kPrepRows, h_hi = G > 1 ? p.H : min(h_lo + kPrepRows, p.H);
   const Chunks c = chunks_of(p, INTER, l);
   const bool rotate = l < (p.rot >> 4);
-  // units of this block: U * 32 heads of a token
-  const int per = G > 1 ? (p.H + U * kPrepRows - 1) / (U * kPrepRows) : 1;
+  // units of this block: 32 heads of a token
+  const int per = G > 1 ? (p.H + kPrepRows - 1) / kPrepRows : 1;
   const int tokens = static_cast<int>(min(static_cast<int64_t>(G), p.T - t0));
-  RawRow next[U], rawk{};
-  auto load = [&](int g, int h0) {
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-      next[i] = load_row(p.q, (t0 + g) * p.H + min(h0 + i * kPrepRows + hw, p.H - 1), c);
-  };
+  RawRow next, rawk{};
+  auto load = [&](int g, int h0) { next = load_row(p.q, (t0 + g) * p.H + min(h0 + hw, p.H - 1), c); };
   load(0, h_lo);
   const bool key = h_lo == 0 && (hw & ~3) < tokens;  // key row of token hw
   int64_t slot = -1;
@@ -246,25 +241,18 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
   load_norm(n, p.q_norm, p.q_weight, p.q_bias, c);
 #pragma unroll 1
   for (int u = 0, g = 0, h0 = h_lo; u < tokens * per; ++u) {
-    RawRow now[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) now[i] = next[i];
-    int g1 = g, h1 = h0 + U * kPrepRows;  // the next unit
+    const RawRow now = next;
+    int g1 = g, h1 = h0 + kPrepRows;  // the next unit
     if (h1 >= h_hi) {
       h1 = h_lo;
       ++g1;
     }
     if (u + 1 < tokens * per) load(g1, h1);
     if (h0 == h_lo) angles(g);
-    if (s_pos[g] >= 0) {  // else padding: nothing is written
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int h = h0 + i * kPrepRows + hw;
-        if (h0 + i * kPrepRows + (hw & ~3) < h_hi)  // warp-uniform
-          finish_row<FP8, INTER>(now[i], n, p.eps, rotate, cs, c, p.q_out, p.q_scale, h < h_hi ? (t0 + g) * p.H + h : -1, l,
-                                  p.status);
-      }
-    }
+    const int h = h0 + hw;
+    if (s_pos[g] >= 0 && h0 + (hw & ~3) < h_hi)  // else padding, or no such heads; the same in all lanes of the warp
+      finish_row<FP8, INTER>(now, n, p.eps, rotate, cs, c, p.q_out, p.q_scale, h < h_hi ? (t0 + g) * p.H + h : -1, l,
+                             p.status);
     g = g1;
     h0 = h1;
   }
@@ -273,7 +261,7 @@ __global__ void __launch_bounds__(kPrepThreads, G > 1 ? 3 : 1) index_prepare_ker
 template <bool FP8, bool INTER, int G>
 cudaError_t launch_groups(const PrepareParams& p, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>((p.T + G - 1) / G), G > 1 ? 1 : (p.H + kPrepRows - 1) / kPrepRows);
-  index_prepare_kernel<FP8, INTER, G, 1><<<grid, kPrepThreads, 0, st>>>(p);
+  index_prepare_kernel<FP8, INTER, G><<<grid, kPrepThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
