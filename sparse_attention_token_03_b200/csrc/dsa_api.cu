@@ -1484,7 +1484,7 @@ int dsa_block_tables(const int32_t* cached_len, const int32_t* new_len, int B, i
   p.status = status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   prof_begin(st);
-  cudaError_t e = launch_block_tables(p, st);
+  cudaError_t e = launch_block_tables(p, sm_count(), st);
   if (e != cudaSuccess) return cuda_fail(e, "block table launch");
   prof_mark(st, "block_tables");
   return DSA_OK;

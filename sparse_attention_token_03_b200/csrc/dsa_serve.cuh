@@ -69,7 +69,7 @@ struct TablesParams {
   int32_t* free_end;          // [1]
   uint32_t* status;           // may be null
 };
-cudaError_t launch_block_tables(const TablesParams& p, cudaStream_t st);
+cudaError_t launch_block_tables(const TablesParams& p, int sms, cudaStream_t st);
 
 struct PrepareParams {
   const uint16_t* q;        // [T][H][128] bf16

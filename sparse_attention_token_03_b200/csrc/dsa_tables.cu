@@ -278,11 +278,11 @@ __global__ void __launch_bounds__(kTabThreadsMax) block_tables_kept_kernel(const
 
 }  // namespace
 
-cudaError_t launch_block_tables(const TablesParams& p, cudaStream_t st) {
+cudaError_t launch_block_tables(const TablesParams& p, int sms, cudaStream_t st) {
   // one thread per request up to the block's limit
   const int threads = p.B <= 256 ? 256 : kTabThreadsMax;
   if (p.B <= kTabKept) {
-    const int grid = std::clamp((p.T_cap + threads - 1) / threads, 1, 148);
+    const int grid = std::clamp((p.T_cap + threads - 1) / threads, 1, std::max(sms, 1));
     const int bytes = (3 * p.B + 2) * static_cast<int>(sizeof(int));
     if (bytes > 40 * 1024) {
       cudaError_t e =
@@ -292,7 +292,7 @@ cudaError_t launch_block_tables(const TablesParams& p, cudaStream_t st) {
     block_tables_kept_kernel<<<grid, threads, bytes, st>>>(p, page_div(p.page_size));
     return cudaGetLastError();
   }
-  const int grid = std::clamp((p.T_cap + 2 * threads - 1) / (2 * threads), 1, 148);  // two rows per thread
+  const int grid = std::clamp((p.T_cap + 2 * threads - 1) / (2 * threads), 1, std::max(sms, 1));  // two rows per thread
   block_tables_kernel<<<grid, threads, 0, st>>>(p);
   return cudaGetLastError();
 }
