@@ -163,7 +163,7 @@ def _native():
             _serve = _load_binding(L)
         except Exception as e:
             warnings.warn(f"the native host side of the serving calls is not available ({e}); their Python checks "
-                          "take over, some 10 to 25 us a call", RuntimeWarning, stacklevel=3)
+                          "take over, some 5 to 20 us more a call", RuntimeWarning, stacklevel=3)
             _serve = _NoBinding
     return _serve
 

@@ -44,10 +44,11 @@
 //
 // What bounds it: with 64 heads the 128-byte wavefronts of shared memory, some
 // 3000 a tile (operands of the MMAs 1920, decoding 576, the rest P, slots and
-// conflicts) in some 4100 cycles against 1970 cycles of MMAs; with few heads
-// the way round a tile buffer (decode, S, softmax, O: some 6000 cycles for two
-// tiles in flight).  999 rows of 64 heads and 2048 entries: 506 us, 563
-// TFLOP/s; 148 rows of 16 heads: 66 us.
+// conflicts: 74% of one a cycle) in some 4100 cycles against 1970 cycles of MMAs;
+// with few heads the way round a tile buffer (decode, S, softmax, O: some 6000
+// cycles for two tiles in flight).  999 rows of 64 heads and 2048 entries: 469 us
+// among other calls, 607 TFLOP/s (492 us in a burst of five: power); 148 rows of
+// 16 heads: 63 us.
 //
 // Numbers: the latents are exact in fp16 (code x scale has 6 significant
 // bits, 2^-10 .. 2688).  Queries go to fp16 too, each row scaled by the power

@@ -81,9 +81,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 }
 
 // tcgen05.mma and tcgen05.commit by one lane (`leader`, from elect_one) under a
-// predicate instead of a branch: the warp stays converged, so descriptors are
-// formed in uniform registers on the way (behind a branch each one is moved
-// there before every MMA, some 60 cycles an MMA instead of 30).
+// predicate instead of a branch, so that the warp stays converged (elect_one has
+// the measured difference).
 template <int kGroup>
 __device__ __forceinline__ void mma_if(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {

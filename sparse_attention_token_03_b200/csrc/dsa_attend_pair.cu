@@ -13,11 +13,11 @@
 //
 // Why pairs: shared memory's 128-byte wavefronts bound these kernels.  64 heads
 // of a block on their own move some 3000 for 64 keys; here 128 keys of 128
-// heads move 3900 per block (operands of the MMAs 1920, decoding 1088, P 128,
-// the rest slots, queries and conflicts) for twice the products, in 5250
-// cycles against 36 x 53 + 16 x 65 = 2950 of MMAs.  2048 rows of 128 heads and
-// 2048 entries: 1.35 ms in a burst of five calls, 867 TFLOP/s (64-head blocks:
-// 2.14 ms).
+// heads move 3800 per block (operands of the MMAs 1920, decoding 1088, P 128,
+// the rest slots, queries and conflicts) for twice the products, in 5470
+// cycles (70% of one a cycle) against 36 x 53 + 16 x 65 = 2950 of MMAs.  2048
+// rows of 128 heads and 2048 entries: 1.49 ms among other calls, 786 TFLOP/s;
+// 1.32 ms in a burst of five (64-head blocks: 2.14).
 //
 //   warps 0-3    softmax and output; a thread has one head and half of the keys
 //                (output dimensions), so maxima and sums need no shuffles
@@ -124,8 +124,9 @@ __device__ __forceinline__ uint32_t in_first(uint32_t bar) {
 // Arrives on a barrier of the cluster's first block.  What the warp wrote to
 // its own block's shared memory is released at cluster scope, since the first
 // block's MMAs read it; the fence is restricted to shared memory.  (With waits
-// to match, 2048 rows of 128 heads take 1.35 ms; 1.24 without the fences, which
-// the PTX memory model does not allow, 1.60 to 1.96 with unrestricted ones.)
+// to match, a burst of 2048 rows of 128 heads takes 1.32 to 1.35 ms; 1.24 without
+// the fences, which the PTX memory model does not allow, 1.60 to 1.96 with
+// unrestricted ones.)
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_bar) {
   asm volatile(
       "fence.release.sync_restrict::shared::cta.cluster;\n\t"

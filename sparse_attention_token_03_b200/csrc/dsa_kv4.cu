@@ -7,8 +7,11 @@
 //
 // with both quotients in fp32, so the stored bytes are a function of the
 // input alone.  A NaN makes its block's scale NaN, so the block reads back as
-// NaN; infinities saturate.  One warp per token, one lane per block: 1152 bytes against
-// 416 per token, bound by HBM (and by the launch for a decode step's rows).
+// NaN; infinities saturate.  One warp per token, one lane per block: 1152 bytes
+// against 416 per token.  Bound by the launch for a decode step's rows and by
+// latency for a chunk: a row's slot is loaded before the row is asked for (16383
+// rows: 11 us written and 10 us read where their bytes take 4 each; warps wait
+// for loads, HBM is at 20% and 9%).
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>

@@ -7,8 +7,7 @@
 //   angle position * inv_freq[i]:  (a cos - b sin, a sin + b cos)
 //   out:    y in bf16, or E4M3 codes of y / scale with scale = max|y| / 448
 //
-// in one pass: 256 bytes read and 256 (or 132) written per row, so HBM bounds
-// it.  A row is 8 lanes of two 8-value chunks, chosen so that both members of
+// in one pass: 256 bytes read and 256 (or 132) written per row.  A row is 8 lanes of two 8-value chunks, chosen so that both members of
 // every rotated pair are in one lane (lane l < rot / 16 of the half-split form
 // holds chunks l and l + rot / 16); statistics are three shuffles.  The angles
 // of a token are shared by all its rows: a block forms those of its tokens
@@ -16,8 +15,10 @@
 // of the fraction of a turn at positions near 10^6; the fraction is then exact
 // enough for fp32 sincospi), and a lane keeps its angles and weights in
 // registers over the rows: read per row, they and the partners' shuffles made
-// the L1 pipe the bound (86%, 163 us for 16384 tokens of 64 heads; now 115 us,
-// 4.7 TB/s).
+// the L1 pipe the bound (86%, 163 us for 16384 tokens of 64 heads; now 110 us,
+// 4.9 TB/s).  What bounds it now is the issue of instructions: the schedulers are
+// busy 63% of all cycles (67% with FP8, some 290 instructions a row of a warp's
+// four), at 3 blocks of 80 registers an SM, while HBM is at 57% (38%).
 // Statistics, rotation and scales are fp32; the store rounds once.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

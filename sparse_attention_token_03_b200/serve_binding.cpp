@@ -1,7 +1,8 @@
 // Host side of the serving operators' Python calls: the argument checks of
 // __init__.py, the output allocations and the call of the C entry point, in
-// one native call.  A decode step's kernels take 1 to 3 us each, and the same
-// checks from Python with ctypes took 8 us a call.
+// one native call.  A decode step's kernels take 1 to 3 us each (attention 20);
+// these calls take the host 3 to 6 us (attention 11), the same checks from Python
+// with ctypes 8 to 27.
 //
 // Every function returns None where an argument is not what the common case
 // takes (a tensor of another type, shape, device or layout, a subclass): the
