@@ -436,10 +436,11 @@ DSA_API int dsa_block_tables(const int32_t* cached_len, const int32_t* new_len, 
  * position * inv_freq[i], (a, b) -> (a cos - b sin, a sin + b cos), where the
  * pair is dimensions (2i, 2i + 1) when `interleaved`, else (i, i + rot / 2).
  * Queries and keys have norms of their own.  Statistics and rotation are
- * fp32, the angle is reduced in fp64 (exact to fp32 at any position); the
- * store rounds once.  The mean under a norm's root plus eps must lie in [2^-100,
- * 2^120): a row outside (magnitudes above some 2^59, or below 2^-49 with an eps
- * below 2^-100) is unspecified and sets status bit 3.
+ * fp32, the angle is reduced in fp64 (for inv_freq up to 1 within 2^-20 of a
+ * radian at any position); the store rounds once.  The mean under a norm's root
+ * plus eps must lie in [2^-100, 2^120): a row outside (magnitudes above some
+ * 2^59, or below 2^-49 with an eps below 2^-100) is unspecified and sets status
+ * bit 3.
  *   q         device, [T][H][128] bf16 (1 <= H <= 256)
  *   k         device, [T][128] bf16
  *   position  device, [T] int32; < 0: padding, neither row is written

@@ -272,7 +272,8 @@ __device__ __forceinline__ void store_query_rows(const uint4 (&v)[R][3], float s
     m[w] = __reduce_max_sync(~0u, max(m[w] & 0xFFFFu, m[w] >> 16));
     const int e = min(141 - static_cast<int>(m[w] >> 7), 126);  // biased exponent field -> shift
     up[w] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-    if (lane == 0) s_c[r[w]] = scale * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // the power of two first: a large scale on a small row may pass fp32 times log2 e
+    if (lane == 0) s_c[r[w]] = scale * __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * kLog2e;
   }
   uint4 now[R], next[R], last[R];
 #pragma unroll

@@ -208,3 +208,14 @@ def test_equal_weights_on_the_longest_list(T, H):
                                   torch.zeros((T, n), dtype=torch.int32, device="cuda"), 1.0, row_seq=zero)
     assert float((out.double() - v).abs().max()) <= v * (2.0 ** -8 + n / 16 * 2.0 ** -23)
     assert float((lse.double() - np.log(n)).abs().max()) <= n / 64 * 2.0 ** -24 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("T,H", [(2, 16), (200, 64), (3, 128)])
+def test_the_largest_scales(T, H):
+    # scores stay moderate: rows of zeros, and rows so small that a scale near fp32's largest brings them back
+    x = make(T, H, 150, ctx=400, seed=T)
+    q = ref.bf16_f64(x["q"]) * 2.0 ** -125
+    q[:, ::3] = 0
+    x["q"] = ref.bf16_bits(q)
+    check(x, scale=3.0e38)
+    check(x, scale=-3.0e38)
